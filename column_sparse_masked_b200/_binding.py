@@ -27,6 +27,10 @@ _SIGS = {
     "flashmask_count_unmasked": (ctypes.c_int, [_P, _P, _P, _P, _DIMS, _P, _P]),
     "flashmask_tile_costs": (ctypes.c_int, [_P, _P, _P, _P, _DIMS, _P, _P]),
     "flashmask_merge_partials": (ctypes.c_int, [_P, _P, ctypes.c_int32, _DIMS, _P, _P, _P]),
+    "flashmask_paged_append": (ctypes.c_int, [_P, _P, _P]),
+    "flashmask_paged_attention_workspace_size": (ctypes.c_size_t, [_P, _P]),
+    "flashmask_paged_attention": (ctypes.c_int, [_P, _P, _P, ctypes.c_size_t, _P]),
+    "flashmask_paged_gather": (ctypes.c_int, [_P, _P, ctypes.c_int32, _P, _P, _P]),
     "flashmask_balance_chunks": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, _P, _P]),
     "flashmask_set_max_ctas": (ctypes.c_int, [ctypes.c_int32]),
     "flashmask_set_bwd_mode": (ctypes.c_int, [ctypes.c_int32]),

@@ -4,7 +4,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <atomic>
 #include <climits>
@@ -18,6 +17,7 @@
 #include <vector>
 
 #include "../../include/flashmask.h"
+#include "api_internal.h"
 #include "common.cuh"
 #include "launchers.h"
 
@@ -45,20 +45,10 @@ int persistent_grid(int64_t n_items, int sm_count) {
   return (int)g;
 }
 
-// NVTX range around an entry point (visible in a profiler's timeline; a no-op
-// when no tool is attached).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
 thread_local char g_last_cuda_error[256] = "";
 std::mutex g_mu;
 
-struct DeviceInfo {
-  int sm_count = 0;
-  int cc = 0;
-  int* status = nullptr;
-};
+}  // namespace
 
 int current_device(DeviceInfo* out) {
   int dev = -1;
@@ -86,6 +76,8 @@ int current_device(DeviceInfo* out) {
   *out = it->second;
   return FLASHMASK_OK;
 }
+
+namespace {
 
 // The library's second stream of the current device, with the fork/join
 // events of one backward call (the mutex serialises their use between host
@@ -130,6 +122,8 @@ AuxStream* aux_stream() {
   return a;
 }
 
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -142,6 +136,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+namespace {
 
 // 4-D map over a [B, N, H, d] bf16 tensor: box = 64 columns x 1 head x box_rows rows.
 int make_map(CUtensorMap* m, const void* ptr, int B, int N, int H, int d, int box_rows = kTile) {
@@ -159,8 +155,6 @@ int make_map(CUtensorMap* m, const void* ptr, int B, int N, int H, int d, int bo
   return FLASHMASK_ERR_CUDA;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 int check_dims(const flashmask_dims* dm) {
   if (!dm) return FLASHMASK_ERR_INVALID_ARG;
   const flashmask_dims& d = *dm;
@@ -174,6 +168,8 @@ int check_dims(const flashmask_dims* dm) {
     return FLASHMASK_ERR_UNSUPPORTED;
   return FLASHMASK_OK;
 }
+
+}  // namespace
 
 int check_masks(const int32_t* lts, const int32_t* lte, const int32_t* uts, const int32_t* ute) {
   if ((lts == nullptr) != (lte == nullptr)) return FLASHMASK_ERR_INVALID_ARG;
@@ -197,12 +193,7 @@ int cuda_status(cudaError_t e, const char* what) {
   return FLASHMASK_ERR_CUDA;
 }
 
-#define FM_TRY(x)                       \
-  do {                                  \
-    int _rc = (x);                      \
-    if (_rc != FLASHMASK_OK) return _rc; \
-  } while (0)
-#define FM_CUDA(x) FM_TRY(cuda_status((x), #x))
+namespace {
 
 float resolve_scale(float scale, int d) { return scale > 0.f ? scale : 1.0f / std::sqrt((float)d); }
 
@@ -825,7 +816,8 @@ const char* flashmask_strerror(int code) {
     case FLASHMASK_ERR_TIMEOUT: return "a device-side bounded wait timed out";
     case FLASHMASK_ERR_NO_DEVICE: return "no sm_100 (B200-class) device is current";
     case FLASHMASK_ERR_BOUNDS:
-      return "a mask value outside [0, Nq] or an internal index out of range (checks build)";
+      return "a page-table entry, position or length of a paged call out of range, or a mask value "
+             "outside [0, Nq] or an internal index out of range (checks build)";
     case FLASHMASK_ERR_TOO_LARGE:
       return "problem too large for flashmask_fwd_noalloc: its forward workspace exceeds "
              "FLASHMASK_NOALLOC_SCRATCH_BYTES (16 MiB); use flashmask_fwd with a workspace";

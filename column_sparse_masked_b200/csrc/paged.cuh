@@ -1,0 +1,80 @@
+// Paged key/value cache: parameter blocks and addressing shared by the append,
+// gather and attention kernels.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+namespace fm {
+
+// Device view of flashmask_pages.  Rows (one token of one head) are numbered
+// page-major: row = (page * Hkv + head) * page_size + slot.
+struct Pages {
+  uint8_t *k, *v;             // rows of row_bytes
+  uint32_t *k_scales, *v_scales;  // bits 4: (scale, minimum) of each row as two bf16; else null
+  const int32_t* table;
+  int64_t table_stride;
+  int B, table_width, num_pages, page_shift, Hkv, d, bits;
+  int row_bytes;              // 2 d, or d / 2 with 4 bits
+  int* status;
+};
+
+struct AppendParams {
+  Pages pg;
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t qs[3], ks[3], vs[3];  // {batch, token, head} strides in elements
+  __nv_bfloat16* q_out;
+  const int32_t *start, *counts, *positions;
+  const float *cos, *sin;
+  int N, Hq, rot, table_len, interleaved;
+};
+
+struct GatherParams {
+  Pages pg;
+  const int32_t* lens;
+  int N;
+  __nv_bfloat16 *k, *v;
+};
+
+struct PagedAttnParams {
+  Pages pg;
+  const __nv_bfloat16* q;
+  int64_t qs[3];
+  const int32_t *lens, *start;
+  const int32_t *lts, *lte, *uts, *ute;
+  int Nq, Hq, Hm, Nm, G, causal;
+  float scale_log2;  // scale * log2(e)
+  __nv_bfloat16* o;
+  float* lse;
+};
+
+__device__ __forceinline__ void record_bounds(int* status) { atomicCAS(status, 0, kDevErrBounds); }
+
+// Page of position j of sequence b; -1 (recorded) for an entry out of range.
+// j must lie in [0, table_width * page_size).
+__device__ __forceinline__ int page_of(const Pages& pg, int b, int j) {
+  const int id = pg.table[b * pg.table_stride + (j >> pg.page_shift)];
+  if ((unsigned)id < (unsigned)pg.num_pages) return id;
+  record_bounds(pg.status);
+  return -1;
+}
+
+__device__ __forceinline__ int64_t row_of(const Pages& pg, int page, int head, int j) {
+  return (((int64_t)page * pg.Hkv + head) << pg.page_shift) + (j & ((1 << pg.page_shift) - 1));
+}
+
+// Cached keys of sequence b: a length beyond the table is recorded and cut.
+__device__ __forceinline__ int checked_len(const Pages& pg, const int32_t* lens, int b) {
+  const int n = lens[b];
+  const int64_t cap = (int64_t)pg.table_width << pg.page_shift;
+  if (n < 0 || n > cap) record_bounds(pg.status);
+  return n < 0 ? 0 : n > cap ? (int)cap : n;
+}
+
+cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st);
+cudaError_t launch_paged_gather(const GatherParams& p, cudaStream_t st);
+cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
+
+}  // namespace fm

@@ -1,0 +1,195 @@
+// Host side of the paged-cache entry points: argument checks and launches.
+#include <climits>
+#include <cmath>
+
+#include "api_internal.h"
+#include "common.cuh"
+#include "launchers.h"
+#include "paged.cuh"
+
+namespace fm {
+namespace {
+
+int check_pages(const flashmask_pages* pg) {
+  if (!pg) return FLASHMASK_ERR_INVALID_ARG;
+  if (pg->B < 0 || pg->table_width < 0 || pg->num_pages < 0 || pg->Hkv <= 0 || pg->table_stride < 0)
+    return FLASHMASK_ERR_INVALID_ARG;
+  if (pg->bits != 16 && pg->bits != 4) return FLASHMASK_ERR_UNSUPPORTED;
+  if (pg->d != 64 && pg->d != 128) return FLASHMASK_ERR_UNSUPPORTED;
+  const int ps = pg->page_size;
+  if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return FLASHMASK_ERR_UNSUPPORTED;
+  // positions, and row numbers of the whole cache, are 32-bit
+  if ((int64_t)pg->table_width * ps > (1 << 30)) return FLASHMASK_ERR_UNSUPPORTED;
+  if ((int64_t)pg->num_pages * pg->Hkv > (int64_t)INT_MAX / ps) return FLASHMASK_ERR_UNSUPPORTED;
+  if (pg->num_pages > 0 && (!pg->k || !pg->v)) return FLASHMASK_ERR_INVALID_ARG;
+  if (pg->bits == 4 && pg->num_pages > 0 && (!pg->k_scales || !pg->v_scales)) return FLASHMASK_ERR_INVALID_ARG;
+  if (pg->B > 0 && pg->table_width > 0 && !pg->table) return FLASHMASK_ERR_INVALID_ARG;
+  if (!aligned16(pg->k) || !aligned16(pg->v) || !aligned16(pg->k_scales) || !aligned16(pg->v_scales))
+    return FLASHMASK_ERR_ALIGN;
+  return FLASHMASK_OK;
+}
+
+// Strided rows: pointer and strides keep every 16-byte load of a row aligned.
+int check_rows(const void* p, const int64_t* strides) {
+  if (!p) return FLASHMASK_ERR_INVALID_ARG;
+  if (!aligned16(p)) return FLASHMASK_ERR_ALIGN;
+  for (int i = 0; i < 3; ++i) {
+    if (strides[i] < 0) return FLASHMASK_ERR_INVALID_ARG;
+    if (strides[i] % 8 != 0) return FLASHMASK_ERR_ALIGN;
+  }
+  return FLASHMASK_OK;
+}
+
+Pages device_pages(const flashmask_pages& pg, const DeviceInfo& di) {
+  Pages p{};
+  p.k = static_cast<uint8_t*>(pg.k);
+  p.v = static_cast<uint8_t*>(pg.v);
+  p.k_scales = static_cast<uint32_t*>(pg.k_scales);
+  p.v_scales = static_cast<uint32_t*>(pg.v_scales);
+  p.table = pg.table;
+  p.table_stride = pg.table_stride;
+  p.B = pg.B;
+  p.table_width = pg.table_width;
+  p.num_pages = pg.num_pages;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < pg.page_size) ++p.page_shift;
+  p.Hkv = pg.Hkv;
+  p.d = pg.d;
+  p.bits = pg.bits;
+  p.row_bytes = pg.bits == 4 ? pg.d / 2 : 2 * pg.d;
+  p.status = di.status;
+  return p;
+}
+
+int check_paged_rows(const flashmask_pages* pg, const flashmask_paged_rows* r) {
+  FM_TRY(check_pages(pg));
+  if (!r) return FLASHMASK_ERR_INVALID_ARG;
+  if (r->Nq < 0 || r->Hq <= 0 || r->Hq % pg->Hkv != 0) return FLASHMASK_ERR_INVALID_ARG;
+  if (r->causal != 0 && r->causal != 1) return FLASHMASK_ERR_INVALID_ARG;
+  FM_TRY(check_masks(r->lts, r->lte, r->uts, r->ute));
+  if (r->lts || r->uts) {
+    if (r->Nm < 0 || (r->Hm != 1 && r->Hm != r->Hq)) return FLASHMASK_ERR_INVALID_ARG;
+  }
+  // work items are numbered in 32 bits
+  if ((int64_t)pg->B * r->Nq * r->Hq > INT_MAX / 4) return FLASHMASK_ERR_UNSUPPORTED;
+  return FLASHMASK_OK;
+}
+
+}  // namespace
+}  // namespace fm
+
+using namespace fm;
+
+extern "C" {
+
+int flashmask_paged_append(const flashmask_pages* pages, const flashmask_append* tokens, void* stream) {
+  NvtxRange nvtx("flashmask_paged_append");
+  FM_TRY(check_pages(pages));
+  if (!tokens) return FLASHMASK_ERR_INVALID_ARG;
+  const flashmask_append& t = *tokens;
+  if (t.N < 0 || t.table_len < 0 || (t.interleaved != 0 && t.interleaved != 1)) return FLASHMASK_ERR_INVALID_ARG;
+  if (t.q && t.Hq <= 0) return FLASHMASK_ERR_INVALID_ARG;
+  if (t.rot < 0 || t.rot > pages->d || t.rot % 16 != 0) return FLASHMASK_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)pages->B * t.N * ((t.q ? t.Hq : 0) + 2 * (int64_t)pages->Hkv);
+  if (rows > INT_MAX) return FLASHMASK_ERR_UNSUPPORTED;
+  if ((int64_t)pages->B * t.N == 0) return FLASHMASK_OK;
+  if (!t.start) return FLASHMASK_ERR_INVALID_ARG;
+  if (t.rot > 0 && (!t.cos || !t.sin)) return FLASHMASK_ERR_INVALID_ARG;
+  if (!aligned16(t.cos) || !aligned16(t.sin)) return FLASHMASK_ERR_ALIGN;
+  FM_TRY(check_rows(t.k, t.k_strides));
+  FM_TRY(check_rows(t.v, t.v_strides));
+  if (t.q) {
+    FM_TRY(check_rows(t.q, t.q_strides));
+    if (!t.q_out) return FLASHMASK_ERR_INVALID_ARG;
+    if (!aligned16(t.q_out)) return FLASHMASK_ERR_ALIGN;
+  }
+  DeviceInfo di;
+  FM_TRY(current_device(&di));
+  AppendParams p{};
+  p.pg = device_pages(*pages, di);
+  p.q = static_cast<const __nv_bfloat16*>(t.q);
+  p.k = static_cast<const __nv_bfloat16*>(t.k);
+  p.v = static_cast<const __nv_bfloat16*>(t.v);
+  for (int i = 0; i < 3; ++i) {
+    p.qs[i] = t.q_strides[i];
+    p.ks[i] = t.k_strides[i];
+    p.vs[i] = t.v_strides[i];
+  }
+  p.q_out = static_cast<__nv_bfloat16*>(t.q_out);
+  p.start = t.start;
+  p.counts = t.counts;
+  p.positions = t.positions;
+  p.cos = t.cos;
+  p.sin = t.sin;
+  p.N = t.N;
+  p.Hq = t.Hq;
+  p.rot = t.rot;
+  p.table_len = t.table_len;
+  p.interleaved = t.interleaved;
+  FM_CUDA(launch_paged_append(p, static_cast<cudaStream_t>(stream)));
+  return FLASHMASK_OK;
+}
+
+size_t flashmask_paged_attention_workspace_size(const flashmask_pages* pages, const flashmask_paged_rows* rows) {
+  if (check_paged_rows(pages, rows) != FLASHMASK_OK) return 0;
+  return 256;
+}
+
+int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_paged_rows* rows, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx("flashmask_paged_attention");
+  FM_TRY(check_paged_rows(pages, rows));
+  const flashmask_paged_rows& r = *rows;
+  if ((int64_t)pages->B * r.Nq == 0) return FLASHMASK_OK;
+  if (!r.lens || !r.o || !r.lse) return FLASHMASK_ERR_INVALID_ARG;
+  FM_TRY(check_rows(r.q, r.q_strides));
+  if (!aligned16(r.o) || !aligned16(r.lse)) return FLASHMASK_ERR_ALIGN;
+  FM_TRY(check_ws(workspace, workspace_bytes, flashmask_paged_attention_workspace_size(pages, rows)));
+  DeviceInfo di;
+  FM_TRY(current_device(&di));
+  PagedAttnParams p{};
+  p.pg = device_pages(*pages, di);
+  p.q = static_cast<const __nv_bfloat16*>(r.q);
+  for (int i = 0; i < 3; ++i) p.qs[i] = r.q_strides[i];
+  p.lens = r.lens;
+  p.start = r.start;
+  p.lts = r.lts;
+  p.lte = r.lte;
+  p.uts = r.uts;
+  p.ute = r.ute;
+  p.Nq = r.Nq;
+  p.Hq = r.Hq;
+  p.Hm = r.Hm;
+  p.Nm = r.lts || r.uts ? r.Nm : 0;
+  p.G = r.Hq / pages->Hkv;
+  p.causal = r.causal;
+  const float scale = r.scale > 0.f ? r.scale : 1.0f / std::sqrt((float)pages->d);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.o = static_cast<__nv_bfloat16*>(r.o);
+  p.lse = r.lse;
+  FM_CUDA(launch_paged_attention(p, static_cast<cudaStream_t>(stream)));
+  return FLASHMASK_OK;
+}
+
+int flashmask_paged_gather(const flashmask_pages* pages, const int32_t* lens, int32_t N, void* k, void* v,
+                           void* stream) {
+  NvtxRange nvtx("flashmask_paged_gather");
+  FM_TRY(check_pages(pages));
+  if (N < 0) return FLASHMASK_ERR_INVALID_ARG;
+  if ((int64_t)pages->B * N > INT_MAX / pages->Hkv) return FLASHMASK_ERR_UNSUPPORTED;
+  if ((int64_t)pages->B * N == 0) return FLASHMASK_OK;
+  if (!lens || !k || !v) return FLASHMASK_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) return FLASHMASK_ERR_ALIGN;
+  DeviceInfo di;
+  FM_TRY(current_device(&di));
+  GatherParams p{};
+  p.pg = device_pages(*pages, di);
+  p.lens = lens;
+  p.N = N;
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  FM_CUDA(launch_paged_gather(p, static_cast<cudaStream_t>(stream)));
+  return FLASHMASK_OK;
+}
+
+}  // extern "C"

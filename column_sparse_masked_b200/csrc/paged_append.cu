@@ -1,0 +1,292 @@
+// Appending to a paged key/value cache (rotation and 4-bit storage on the way)
+// and gathering pages into dense tensors.  Both move bytes: a row (one token
+// of one head) is read once and written once, and the arithmetic in between
+// has to stay below the time that takes.
+#include <cuda_bf16.h>
+
+#include "launchers.h"
+#include "paged.cuh"
+#include "sm100_primitives.cuh"
+
+namespace fm {
+namespace {
+
+// 16 values of one row as fp32, from two 16-byte chunks at offsets a and b.
+__device__ __forceinline__ void load_chunks(const __nv_bfloat16* row, int a, int b, float (&x)[16]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(row + a), w = *reinterpret_cast<const uint4*>(row + b);
+  const uint32_t r[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = __uint_as_float(r[i] << 16);
+    x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ void pack_chunks(const float (&x)[16], uint32_t (&r)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+}
+
+__device__ __forceinline__ void store_chunks(__nv_bfloat16* row, int a, int b, const uint32_t (&r)[8]) {
+  *reinterpret_cast<uint4*>(row + a) = make_uint4(r[0], r[1], r[2], r[3]);
+  *reinterpret_cast<uint4*>(row + b) = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// a c - b s rounded to fp32 once (to within 2^-47 of the exact value before
+// that): products and their difference carried with their rounding errors
+// (Dekker and Knuth's error-free product and sum).  Rows stored in 4 bits need
+// it: where a rotated value lands next to the middle of two bf16 values, and
+// so of two codes, the rounding of the products must not decide.
+__device__ __forceinline__ float cross_exact(float a, float c, float b, float s) {
+  const float p = a * c, ep = fmaf(a, c, -p);
+  const float r = -(b * s), er = fmaf(-b, s, -r);
+  const float t = p + r, z = t - p;
+  const float et = (p - (t - z)) + (r - z);
+  return t + ((ep + er) + et);
+}
+
+template <bool EXACT>
+__device__ __forceinline__ void rotate_pair(float& x, float& y, float c, float s) {
+  const float x1 = x, x2 = y;
+  if (EXACT) {
+    x = cross_exact(x1, c, x2, s);
+    y = cross_exact(x2, c, -x1, s);
+  } else {
+    x = fmaf(x1, c, -(x2 * s));
+    y = fmaf(x2, c, x1 * s);
+  }
+}
+
+// Chunk a holds pairs' first values and chunk b their second (halves), or each
+// holds four whole pairs (neighbours).
+template <bool EXACT>
+__device__ __forceinline__ void rotate(float (&x)[16], const float (&c)[8], const float (&s)[8], bool interleaved) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (interleaved)
+      rotate_pair<EXACT>(x[2 * i], x[2 * i + 1], c[i], s[i]);
+    else
+      rotate_pair<EXACT>(x[i], x[i + 8], c[i], s[i]);
+  }
+}
+
+// The code of x in a row with minimum lo: the integer nearest to (x - lo) /
+// scale, ties to even.  The quotient only proposes; the decision at k + 1/2 is
+// the sign of (x - lo) - (k + 1/2) scale, which fp32 gives without error (the
+// product has 13 bits, and the difference x - lo comes with its rounding
+// error), so that no rounding moves a value across the middle of two codes.
+__device__ __forceinline__ uint32_t code_of(float x, float lo, float scale, float inv) {
+  const float diff = x - lo, z = diff - x;
+  const float err = (x - (diff - z)) + (-lo - z);
+  const float k = fminf(floorf(diff * inv), 15.f);
+  const float r = fmaf(-scale, k + 0.5f, diff) + err;
+  const uint32_t ki = (uint32_t)k;
+  return min(ki + ((r > 0.f || (r == 0.f && (ki & 1u))) ? 1u : 0u), 15u);
+}
+
+// One thread takes 16 values of a row (two 16-byte chunks that hold whole
+// pairs), D/16 neighbouring lanes a row, and goes through rows of one token
+// `gpt` apart with that token's cosines and sines in registers.
+template <int D, int BITS>
+__global__ void __launch_bounds__(128) paged_append_kernel(AppendParams p, int gpt_log2) {
+  constexpr int L = D / 16;
+  const int lane = threadIdx.x & 31, e = lane & (L - 1);
+  const unsigned gmask = ((1u << L) - 1u) << (lane & ~(L - 1));
+  const int64_t group = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) / L;
+  const int64_t token = group >> gpt_log2;
+  const int g0 = (int)(group & ((1 << gpt_log2) - 1));
+  if (token >= (int64_t)p.pg.B * p.N) return;
+  const int b = (int)(token / p.N), i = (int)(token % p.N);
+
+  int count = p.N;
+  if (p.counts) {
+    count = p.counts[b];
+    if (count < 0 || count > p.N) {
+      if (i == 0 && g0 == 0 && e == 0) record_bounds(p.pg.status);
+      count = min(max(count, 0), p.N);
+    }
+  }
+  const bool real = i < count;
+  // where the token goes, and by which angles it turns
+  const int64_t pos = (int64_t)p.start[b] + i;
+  bool turn_ok = real, store_ok = real;
+  int page = -1;
+  float c[8], s[8];
+  const bool turns = e < p.rot / 16;
+  if (real) {
+    if (pos < 0 || pos >= (int64_t)p.pg.table_width << p.pg.page_shift) {
+      record_bounds(p.pg.status);
+      store_ok = false;
+    } else {
+      page = page_of(p.pg, b, (int)pos);
+      store_ok = page >= 0;
+    }
+    if (p.rot > 0) {
+      const int64_t r = p.positions ? (int64_t)p.positions[token] : pos;
+      if (r < 0 || r >= p.table_len) {
+        record_bounds(p.pg.status);
+        turn_ok = store_ok = false;
+      } else if (turns) {
+        const float4* cp = reinterpret_cast<const float4*>(p.cos + r * (p.rot / 2) + 8 * e);
+        const float4* sp = reinterpret_cast<const float4*>(p.sin + r * (p.rot / 2) + 8 * e);
+        const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
+        c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w; c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
+        s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+      }
+    }
+  }
+  // offsets of the two chunks
+  int a = 16 * e, bo = 16 * e + 8;
+  if (turns && !p.interleaved) {
+    a = 8 * e;
+    bo = p.rot / 2 + 8 * e;
+  }
+  const int Hq = p.q ? p.Hq : 0, rows = Hq + 2 * p.pg.Hkv;
+  for (int r = g0; r < rows; r += 1 << gpt_log2) {
+    float x[16];
+    uint32_t w[8];
+    if (r < Hq) {
+      __nv_bfloat16* out = p.q_out + (token * Hq + r) * D;
+      if (turn_ok) {
+        load_chunks(p.q + b * p.qs[0] + i * p.qs[1] + r * p.qs[2], a, bo, x);
+        if (turns) rotate<false>(x, c, s, p.interleaved);
+        pack_chunks(x, w);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 0u;
+      }
+      store_chunks(out, a, bo, w);
+      continue;
+    }
+    if (!store_ok) continue;
+    const bool is_k = r < Hq + p.pg.Hkv;
+    const int h = is_k ? r - Hq : r - Hq - p.pg.Hkv;
+    const __nv_bfloat16* src =
+        is_k ? p.k + b * p.ks[0] + i * p.ks[1] + h * p.ks[2] : p.v + b * p.vs[0] + i * p.vs[1] + h * p.vs[2];
+    load_chunks(src, a, bo, x);
+    if (is_k && turns) rotate<BITS == 4>(x, c, s, p.interleaved);
+    pack_chunks(x, w);
+    const int64_t row = row_of(p.pg, page, h, (int)pos);
+    uint8_t* dst = (is_k ? p.pg.k : p.pg.v) + row * (BITS == 4 ? D / 2 : 2 * D);
+    if (BITS == 16) {
+      store_chunks(reinterpret_cast<__nv_bfloat16*>(dst), a, bo, w);
+      continue;
+    }
+    float lo = INFINITY, hi = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      lo = fminf(lo, fminf(x[2 * j], x[2 * j + 1]));
+      hi = fmaxf(hi, fmaxf(x[2 * j], x[2 * j + 1]));
+      bad |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+    }
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(gmask, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(gmask, hi, o));
+    }
+    const float spread = hi - lo;
+    bad = __any_sync(gmask, bad) || spread == INFINITY;
+    const uint32_t sm = bad ? 0x7fff7fffu : pack_bf16x2(__fdiv_rn(spread, 15.f), lo);
+    float scale = __uint_as_float(sm << 16);
+    uint32_t w0 = 0u, w1 = 0u;
+    if (scale > 0.f) {  // false for a row of equal values and for NaN
+      // tiny scales have no reciprocal: the row is scaled by a power of two
+      const float up = scale < 0x1p-100f ? 0x1p64f : 1.f;
+      scale *= up;
+      lo *= up;
+      const float inv = 1.f / scale;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w0 |= code_of(x[j] * up, lo, scale, inv) << (4 * j);
+        w1 |= code_of(x[8 + j] * up, lo, scale, inv) << (4 * j);
+      }
+    }
+    *reinterpret_cast<uint32_t*>(dst + a / 2) = w0;
+    *reinterpret_cast<uint32_t*>(dst + bo / 2) = w1;
+    if (e == 0) (is_k ? p.pg.k_scales : p.pg.v_scales)[row] = sm;
+  }
+}
+
+// One thread writes 16 values of k and of v (32-byte stores, whole rows by
+// D/16 lanes): neighbouring lanes take neighbouring heads of one token, as the
+// output has them.
+template <int D, int BITS>
+__global__ void __launch_bounds__(256) paged_gather_kernel(GatherParams p, int64_t total) {
+  constexpr int L = D / 16;
+  const int64_t t = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  if (t >= total) return;
+  const int e = (int)(t % L);
+  const int64_t out_row = t / L;  // (b, j, h)
+  const int h = (int)(out_row % p.pg.Hkv);
+  const int64_t bj = out_row / p.pg.Hkv;
+  const int b = (int)(bj / p.N), j = (int)(bj % p.N);
+  uint32_t wk[8] = {}, wv[8] = {};
+  if (j < checked_len(p.pg, p.lens, b)) {
+    const int page = page_of(p.pg, b, j);
+    if (page >= 0) {
+      const int64_t row = row_of(p.pg, page, h, j);
+      if (BITS == 16) {
+        const uint4* sk = reinterpret_cast<const uint4*>(p.pg.k + row * (2 * D) + 32 * e);
+        const uint4* sv = reinterpret_cast<const uint4*>(p.pg.v + row * (2 * D) + 32 * e);
+        const uint4 k0 = sk[0], k1 = sk[1], v0 = sv[0], v1 = sv[1];
+        wk[0] = k0.x; wk[1] = k0.y; wk[2] = k0.z; wk[3] = k0.w; wk[4] = k1.x; wk[5] = k1.y; wk[6] = k1.z; wk[7] = k1.w;
+        wv[0] = v0.x; wv[1] = v0.y; wv[2] = v0.z; wv[3] = v0.w; wv[4] = v1.x; wv[5] = v1.y; wv[6] = v1.z; wv[7] = v1.w;
+      } else {
+        const uint2 ck = *reinterpret_cast<const uint2*>(p.pg.k + row * (D / 2) + 8 * e);
+        const uint2 cv = *reinterpret_cast<const uint2*>(p.pg.v + row * (D / 2) + 8 * e);
+        const uint32_t ks = p.pg.k_scales[row], vs = p.pg.v_scales[row];
+        const float k_s = __uint_as_float(ks << 16), k_m = __uint_as_float(ks & 0xffff0000u);
+        const float v_s = __uint_as_float(vs << 16), v_m = __uint_as_float(vs & 0xffff0000u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // scale * code has 12 bits: the sum is rounded to fp32 once, then to bf16
+          const uint32_t c = (i < 4 ? ck.x : ck.y) >> (8 * (i & 3)), f = (i < 4 ? cv.x : cv.y) >> (8 * (i & 3));
+          wk[i] = pack_bf16x2(fmaf(k_s, (float)(c & 15u), k_m), fmaf(k_s, (float)((c >> 4) & 15u), k_m));
+          wv[i] = pack_bf16x2(fmaf(v_s, (float)(f & 15u), v_m), fmaf(v_s, (float)((f >> 4) & 15u), v_m));
+        }
+      }
+    }
+  }
+  st_global_v8_na(p.k + out_row * D + 16 * e, wk);
+  st_global_v8_na(p.v + out_row * D + 16 * e, wv);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st) {
+  const int64_t tokens = (int64_t)p.pg.B * p.N;
+  if (tokens == 0) return cudaSuccess;
+  const int L = p.pg.d / 16, rows = (p.q ? p.Hq : 0) + 2 * p.pg.Hkv;
+  int gl = 0;  // lane groups per token (log2): one a row
+  while ((1 << gl) < rows && (1 << gl) < 128 / L) ++gl;
+  const int64_t threads = (tokens << gl) * L;
+  const unsigned blocks = (unsigned)((threads + 127) / 128);
+  note_launch();
+  if (p.pg.d == 128) {
+    if (p.pg.bits == 4) paged_append_kernel<128, 4><<<blocks, 128, 0, st>>>(p, gl);
+    else paged_append_kernel<128, 16><<<blocks, 128, 0, st>>>(p, gl);
+  } else {
+    if (p.pg.bits == 4) paged_append_kernel<64, 4><<<blocks, 128, 0, st>>>(p, gl);
+    else paged_append_kernel<64, 16><<<blocks, 128, 0, st>>>(p, gl);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_gather(const GatherParams& p, cudaStream_t st) {
+  const int64_t total = (int64_t)p.pg.B * p.N * p.pg.Hkv * (p.pg.d / 16);
+  if (total == 0) return cudaSuccess;
+  const unsigned blocks = (unsigned)((total + 255) / 256);
+  note_launch();
+  if (p.pg.d == 128) {
+    if (p.pg.bits == 4) paged_gather_kernel<128, 4><<<blocks, 256, 0, st>>>(p, total);
+    else paged_gather_kernel<128, 16><<<blocks, 256, 0, st>>>(p, total);
+  } else {
+    if (p.pg.bits == 4) paged_gather_kernel<64, 4><<<blocks, 256, 0, st>>>(p, total);
+    else paged_gather_kernel<64, 16><<<blocks, 256, 0, st>>>(p, total);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace fm

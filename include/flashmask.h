@@ -67,8 +67,9 @@ extern "C" {
 #define FLASHMASK_ERR_TIMEOUT (-6)     /* a kernel's bounded wait expired (status word)   */
 #define FLASHMASK_ERR_NO_DEVICE (-7)   /* no sm_100 device current                        */
 #define FLASHMASK_ERR_TOO_LARGE (-8)   /* problem needs more than the static no-alloc scratch */
-#define FLASHMASK_ERR_BOUNDS (-9)      /* checks build: mask value outside [0, Nq], or an internal
-                                          index out of range (status word)                   */
+#define FLASHMASK_ERR_BOUNDS (-9)      /* status word: a paged call met a bad table entry, position or
+                                          length; checks build: mask value outside [0, Nq], or an
+                                          internal index out of range                        */
 
 /* Problem shape.  B batch, Hq query heads, Hkv key/value heads, Hm mask heads
  * (1 or Hq), Nq query rows, Nk key columns, d head dimension. */
@@ -263,6 +264,112 @@ int flashmask_tile_costs(const int32_t* lts, const int32_t* lte, const int32_t* 
  * cost or a total above INT64_MAX / 4.
  */
 int flashmask_balance_chunks(const int64_t* costs, int32_t n, int32_t parts, int32_t* bounds, int64_t* max_cost);
+
+/*
+ * Paged key/value cache
+ * ---------------------
+ * Serving a model trained with these masks: keys and values live in pages of
+ * `page_size` tokens that a table hands to sequences.  (No counterpart in the
+ * paper, which trains; the mask encoding is the same.)
+ *
+ *   k, v      bits 16: bf16 [num_pages, Hkv, page_size, d]
+ *             bits 4:  uint8 [num_pages, Hkv, page_size, d / 2]; byte i of a
+ *                      row holds the codes (0..15) of values 2i (low half)
+ *                      and 2i + 1
+ *   k_scales, v_scales   bits 4: bf16 [num_pages, Hkv, page_size, 2], the scale
+ *                      and the minimum of each row: a code c stands for
+ *                      minimum + scale * c.  bits 16: NULL.
+ *   table     int32 [B, table_width], rows table_stride apart: position j of
+ *             sequence b is slot j % page_size of page table[b][j / page_size]
+ *
+ * A token's row of one head is contiguous and so are the rows of one head in
+ * a page, so that one copy brings a head's part of a page.  Sequences may
+ * share pages that are only read.  d in {64, 128}; page_size in {16, 32, 64,
+ * 128, 256}.  Table entries and lengths are device data that the host cannot
+ * check: an entry outside [0, num_pages) that a call would use, and a length
+ * beyond table_width * page_size, are recorded as FLASHMASK_ERR_BOUNDS in the
+ * status word (in every build) and no access is made with them.
+ */
+typedef struct flashmask_pages {
+  void *k, *v, *k_scales, *v_scales;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t B, table_width, num_pages, page_size, Hkv, d, bits;
+} flashmask_pages;
+
+/* Tokens to append: q, k, v are bf16 [B, N, heads, d] with unit stride over d
+ * and strides {batch, token, head} in elements (multiples of 8; 16-byte
+ * aligned pointers), as views of a fused projection are. */
+typedef struct flashmask_append {
+  const void *q, *k, *v; /* q may be NULL (Hq is then ignored) */
+  int64_t q_strides[3], k_strides[3], v_strides[3];
+  void* q_out;              /* bf16 [B, N, Hq, d] contiguous; may be q itself where q is contiguous */
+  const int32_t* start;     /* [B]: position of each sequence's first new token */
+  const int32_t* counts;    /* [B]: how many of the N tokens are real (NULL: all) */
+  const int32_t* positions; /* [B, N]: rotation position of each token (NULL: start + i) */
+  const float *cos, *sin;   /* [table_len, rot / 2] (NULL with rot 0: no rotation) */
+  int32_t N, Hq, rot, table_len, interleaved;
+} flashmask_append;
+
+/*
+ * Appends N new tokens per sequence: token i of sequence b goes to position
+ * start[b] + i.  On the way the first `rot` values (a multiple of 16, at most
+ * d) of each row of q and k are rotated by the angles of the token's rotation
+ * position r: each pair (x1, x2) becomes (x1 c - x2 s, x2 c + x1 s) with
+ * c = cos[r][i], s = sin[r][i], where pair i is values (i, i + rot/2), or
+ * (2i, 2i + 1) with `interleaved`.  The rotated q is written to q_out (rows at
+ * or past counts[b] as 0), k and v into their pages; v is not rotated.
+ * Rotated values are rounded once, to bf16.  With bits 4 each bf16 row x is
+ * stored as minimum = min x, scale = bf16((max x - min x) / 15) and the codes
+ * nearest to (x - minimum) / scale (ties to even, at most 15); a row with a
+ * NaN or an infinity, or whose spread overflows fp32, reads back as NaN.
+ *
+ * Slots behind a sequence's last token are left as they were.  Positions
+ * outside the table, bad table entries and rotation positions outside
+ * [0, table_len) are recorded as FLASHMASK_ERR_BOUNDS; such a token is not
+ * stored, and its q row (rotation position) is written as 0.  The slots that
+ * one call writes must be distinct.
+ */
+int flashmask_paged_append(const flashmask_pages* pages, const flashmask_append* tokens, void* stream);
+
+/* Rows that attend to a paged cache. */
+typedef struct flashmask_paged_rows {
+  const void* q;        /* bf16 [B, Nq, Hq, d], strides as in flashmask_append */
+  int64_t q_strides[3];
+  const int32_t* lens;  /* [B]: cached keys of each sequence */
+  const int32_t* start; /* [B]: position of each sequence's first row (NULL: lens - Nq) */
+  const int32_t *lts, *lte, *uts, *ute; /* [B, Hm, Nm]; a NULL pair = empty intervals */
+  int32_t Nq, Hq, Hm, Nm;
+  int32_t causal;       /* 1: a row at position p sees keys j <= p only; 0: all keys */
+  float scale;          /* <= 0: 1/sqrt(d) */
+  void* o;              /* bf16 [B, Nq, Hq, d] contiguous */
+  float* lse;           /* fp32 [B, Hq, Nq] */
+} flashmask_paged_rows;
+
+/*
+ * Attention of a few rows per sequence (single tokens, drafted runs) over a
+ * paged cache, O and LSE as flashmask_fwd.  Row i of sequence b stands at
+ * position p = start[b] + i and sees key j iff j < lens[b], j <= p (causal),
+ * and neither LTS[j] <= p < LTE[j] nor UTS[j] <= p < UTE[j]; keys at or past
+ * Nm have empty intervals.  Rows with no visible key give O = 0, LSE = -inf.
+ * Keys that a row does not see have no influence on it, whatever they hold
+ * (NaN included).  With bits 4 the codes enter the products as they are
+ * and the scales and minima are applied to sums in fp32.
+ * Any Nq >= 0; a long chunk of rows is better served by flashmask_paged_gather
+ * and flashmask_fwd.  The result does not depend on what other sequences hold
+ * beyond fp32 summation order; equal calls give equal bits.
+ */
+size_t flashmask_paged_attention_workspace_size(const flashmask_pages* pages, const flashmask_paged_rows* rows);
+int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_paged_rows* rows, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Pages as dense keys and values, k and v bf16 [B, N, Hkv, d] contiguous (what
+ * flashmask_fwd and flashmask_bwd take): rows j < min(lens[b], N) from the
+ * pages (bits 4: minimum + scale * code, rounded to bf16), the others 0.
+ */
+int flashmask_paged_gather(const flashmask_pages* pages, const int32_t* lens, int32_t N, void* k, void* v,
+                           void* stream);
 
 /* Selects the backward mode (FLASHMASK_BWD_FUSED or FLASHMASK_BWD_SPLIT) for
  * every later flashmask_bwd call of the process; FLASHMASK_ERR_INVALID_ARG
