@@ -388,7 +388,8 @@ def get_status() -> int:
 
 ERR_BOUNDS = -9
 
-_TIMEOUT_KERNELS = ("forward", "backward key side", "backward query side", "wait self-test", "fused backward")
+_TIMEOUT_KERNELS = ("forward", "backward key side", "backward query side", "wait self-test", "fused backward",
+                    "paged attention")
 
 
 def get_timeout_info() -> dict:

@@ -42,6 +42,13 @@ int cuda_status(cudaError_t e, const char* what);
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
+// Persistent grid of an attention kernel: one CTA per SM, at most one per
+// work item, at most the process-wide cap when one is set.
+int persistent_grid(int64_t n_items, int sm_count);
+
+// Limit of every bounded device-side wait (flashmask_set_wait_limit_ns).
+uint64_t wait_limit_ns();
+
 #define FM_TRY(x)                       \
   do {                                  \
     int _rc = (x);                      \

@@ -36,8 +36,11 @@ std::atomic<int> g_max_ctas{0};  // 0: one persistent CTA per SM
 std::atomic<int> g_bwd_mode{FLASHMASK_BWD_FUSED};
 std::atomic<int> g_fwd_pairing{1};
 
-// Persistent grid of an attention kernel: one CTA per SM, at most one per
-// work item, at most the process-wide cap when one is set.
+thread_local char g_last_cuda_error[256] = "";
+std::mutex g_mu;
+
+}  // namespace
+
 int persistent_grid(int64_t n_items, int sm_count) {
   int64_t g = n_items < sm_count ? n_items : sm_count;
   const int cap = g_max_ctas.load(std::memory_order_relaxed);
@@ -45,10 +48,7 @@ int persistent_grid(int64_t n_items, int sm_count) {
   return (int)g;
 }
 
-thread_local char g_last_cuda_error[256] = "";
-std::mutex g_mu;
-
-}  // namespace
+uint64_t wait_limit_ns() { return (uint64_t)g_wait_limit_ns.load(); }
 
 int current_device(DeviceInfo* out) {
   int dev = -1;

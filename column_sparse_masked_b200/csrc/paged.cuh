@@ -2,6 +2,7 @@
 // gather and attention kernels.
 #pragma once
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -48,7 +49,25 @@ struct PagedAttnParams {
   float scale_log2;  // scale * log2(e)
   __nv_bfloat16* o;
   float* lse;
+  // work: groups (a sequence, or a sequence and KV head with per-head masks) of `mult` items of `rows` rows
+  int per_head, n_groups, mult, n_rb, rows, tile_keys;
+  int min_tiles;            // units that a run holds at least
+  // plan (with mask vectors): visible tiles of each group, row-visibility words of each key
+  const int* counts;        // [n_groups]
+  const int* list;          // [n_groups, list_stride]: tile << 1 | some pair hidden
+  int list_stride;
+  const uint32_t* words;    // [B, Hm, n_words, words_stride]: bit i = row 32 w + i sees the key
+  int n_words;
+  int64_t words_stride;
+  int words_shared;         // one word per key serves all rows: loaded with the tile
+  // partial sums of cut items: two slots per CTA
+  float* part;              // [2 grid, rows, d]
+  float2* stat;             // [2 grid, rows]: running maximum, sum
+  int* meta;                // [grid, 8]: the item that begins in a CTA's run and goes on in the next
+  uint64_t wait_limit_ns;
 };
+
+constexpr int kPagedMaxCtas = 160;
 
 __device__ __forceinline__ void record_bounds(int* status) { atomicCAS(status, 0, kDevErrBounds); }
 
@@ -75,6 +94,9 @@ __device__ __forceinline__ int checked_len(const Pages& pg, const int32_t* lens,
 
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st);
 cudaError_t launch_paged_gather(const GatherParams& p, cudaStream_t st);
-cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
+int paged_tile_keys(int d, int bits);
+// Plan (when p.list is set; counts, list and words are its writable views), attention and merge.
+cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                                   int* counts, int* list, uint32_t* words, cudaStream_t st);
 
 }  // namespace fm

@@ -75,6 +75,54 @@ int check_paged_rows(const flashmask_pages* pg, const flashmask_paged_rows* r) {
   return FLASHMASK_OK;
 }
 
+// Work split and workspace of an attention call.
+struct PagedLayout {
+  int per_head, n_groups, mult, n_rb, rows, tile_keys, n_words;
+  int64_t keys;  // capacity of the table, in whole tiles
+  size_t part, stat, meta, counts, list, words, bytes;
+};
+
+PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& r) {
+  PagedLayout L{};
+  const bool masked = r.lts || r.uts;
+  const int64_t R = (int64_t)r.Nq * (r.Hq / pg.Hkv);
+  L.rows = R <= 8 ? 8 : R <= 16 ? 16 : 32;
+  L.n_rb = (int)((R + L.rows - 1) / L.rows);
+  L.per_head = masked && r.Hm > 1;
+  L.n_groups = L.per_head ? pg.B * pg.Hkv : pg.B;
+  L.mult = L.per_head ? L.n_rb : pg.Hkv * L.n_rb;
+  L.tile_keys = paged_tile_keys(pg.d, pg.bits);
+  L.n_words = (r.Nq + 31) / 32;
+  const int64_t cap = (int64_t)pg.table_width * pg.page_size;
+  L.keys = (cap + L.tile_keys - 1) / L.tile_keys * L.tile_keys;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t o = off; off = ws_align(off + bytes); return o; };
+  L.part = take((size_t)2 * kPagedMaxCtas * L.rows * pg.d * 4);
+  L.stat = take((size_t)2 * kPagedMaxCtas * L.rows * 8);
+  L.meta = take((size_t)kPagedMaxCtas * 8 * 4);
+  if (masked) {
+    L.counts = take((size_t)L.n_groups * 4);
+    L.list = take((size_t)L.n_groups * (L.keys / L.tile_keys) * 4);
+    L.words = take((size_t)pg.B * r.Hm * L.n_words * L.keys * 4);
+  }
+  L.bytes = off;
+  return L;
+}
+
+// 2-D map over the rows of all pages: box = 64 values x box_rows rows, 128-byte swizzle.
+int make_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int d, int box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return FLASHMASK_ERR_CUDA;
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FLASHMASK_OK : cuda_status(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+}
+
 }  // namespace
 }  // namespace fm
 
@@ -132,7 +180,7 @@ int flashmask_paged_append(const flashmask_pages* pages, const flashmask_append*
 
 size_t flashmask_paged_attention_workspace_size(const flashmask_pages* pages, const flashmask_paged_rows* rows) {
   if (check_paged_rows(pages, rows) != FLASHMASK_OK) return 0;
-  return 256;
+  return paged_layout(*pages, *rows).bytes;
 }
 
 int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_paged_rows* rows, void* workspace,
@@ -144,9 +192,11 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
   if (!r.lens || !r.o || !r.lse) return FLASHMASK_ERR_INVALID_ARG;
   FM_TRY(check_rows(r.q, r.q_strides));
   if (!aligned16(r.o) || !aligned16(r.lse)) return FLASHMASK_ERR_ALIGN;
-  FM_TRY(check_ws(workspace, workspace_bytes, flashmask_paged_attention_workspace_size(pages, rows)));
+  const PagedLayout L = paged_layout(*pages, r);
+  FM_TRY(check_ws(workspace, workspace_bytes, L.bytes));
   DeviceInfo di;
   FM_TRY(current_device(&di));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   PagedAttnParams p{};
   p.pg = device_pages(*pages, di);
   p.q = static_cast<const __nv_bfloat16*>(r.q);
@@ -157,17 +207,48 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
   p.lte = r.lte;
   p.uts = r.uts;
   p.ute = r.ute;
+  const bool masked = r.lts || r.uts;
   p.Nq = r.Nq;
   p.Hq = r.Hq;
-  p.Hm = r.Hm;
-  p.Nm = r.lts || r.uts ? r.Nm : 0;
+  p.Hm = masked ? r.Hm : 1;
+  p.Nm = masked ? r.Nm : 0;
   p.G = r.Hq / pages->Hkv;
   p.causal = r.causal;
   const float scale = r.scale > 0.f ? r.scale : 1.0f / std::sqrt((float)pages->d);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.o = static_cast<__nv_bfloat16*>(r.o);
   p.lse = r.lse;
-  FM_CUDA(launch_paged_attention(p, static_cast<cudaStream_t>(stream)));
+  p.per_head = L.per_head;
+  p.n_groups = L.n_groups;
+  p.mult = L.mult;
+  p.n_rb = L.n_rb;
+  p.rows = L.rows;
+  p.tile_keys = L.tile_keys;
+  p.min_tiles = 8;
+  p.part = reinterpret_cast<float*>(ws + L.part);
+  p.stat = reinterpret_cast<float2*>(ws + L.stat);
+  p.meta = reinterpret_cast<int*>(ws + L.meta);
+  int *counts = nullptr, *list = nullptr;
+  uint32_t* words = nullptr;
+  if (masked) {
+    p.counts = counts = reinterpret_cast<int*>(ws + L.counts);
+    p.list = list = reinterpret_cast<int*>(ws + L.list);
+    p.words = words = reinterpret_cast<uint32_t*>(ws + L.words);
+    p.list_stride = (int)(L.keys / L.tile_keys);
+    p.n_words = L.n_words;
+    p.words_stride = L.keys;
+    p.words_shared = p.Hm == 1 && L.n_words == 1;
+  }
+  p.wait_limit_ns = wait_limit_ns();
+  CUtensorMap tk{}, tv{};
+  if (pages->bits == 16 && pages->num_pages > 0) {
+    const int box = pages->page_size < L.tile_keys ? pages->page_size : L.tile_keys;
+    const int64_t rows = (int64_t)pages->num_pages * pages->Hkv * pages->page_size;
+    FM_TRY(make_rows_map(&tk, pages->k, rows, pages->d, box));
+    FM_TRY(make_rows_map(&tv, pages->v, rows, pages->d, box));
+  }
+  const int grid = persistent_grid(kPagedMaxCtas, di.sm_count);
+  FM_CUDA(launch_paged_attention(p, tk, tv, grid, counts, list, words, static_cast<cudaStream_t>(stream)));
   return FLASHMASK_OK;
 }
 

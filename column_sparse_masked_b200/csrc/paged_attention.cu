@@ -1,92 +1,1112 @@
-// Attention over a paged key/value cache: one warp per row.
+// Attention of a few rows per sequence over a paged key/value cache.
+//
+// The rows of one KV head (new tokens x the q-heads that share it) read every
+// visible key and value once and do 4 d FLOP with each: bytes bound it as long
+// as a block holds at most some 32 rows, so the design is about keeping the
+// memory system full and the work even.
+//
+//  - Work.  An item is (sequence, KV head, block of 8, 16 or 32 rows); its
+//    units are its tiles of 32 or 64 keys.  All units are laid end to end and
+//    every CTA (one per SM) takes an equal run of them, whatever the lengths
+//    of the sequences: a run may end one item, hold several and begin another.
+//    An item inside one run is finished there; one that is cut leaves fp32
+//    partial sums, which a second kernel joins in a fixed order (no atomics:
+//    equal calls give equal bits).  Lengths are device data and the grid does
+//    not depend on them, so a captured graph serves growing sequences.
+//  - Masks.  With mask vectors a plan kernel runs first: it turns each key's
+//    four boundaries into one bit per row, and lists the tiles that some row
+//    sees, so hidden tiles are neither read nor counted as work.
+//  - Loads.  One warp looks pages up and fills a ring of tiles in shared
+//    memory by TMA (swizzled boxes for bf16, plain bulk copies for 4 bits);
+//    the ring spans items, so the loads never pause at an item's end.
+//  - Products.  Tensor cores with the keys as the M side (mma m16n8k16): S^T =
+//    K Q^T and O^T = V^T P^T need only 8 row columns, where the usual
+//    orientation pads the rows to 16.  mma.sync and not tcgen05: rows are
+//    few, P never leaves registers, and the tensor pipe is far from the bound.
+//    Each warp keeps its own running maximum and sums over its tiles; warps
+//    meet once per item.
+//  - 4 bits.  A row's codes enter the products as the integers code - 8 (exact
+//    in bf16); scale and minimum are applied to sums in fp32:
+//      q.k = s (q.(c - 8)) + (m + 8 s) sum(q)
+//      o   = sum (p s)(c - 8) + sum p (m + 8 s)
+//    The contraction may run over the head's values in any order as long as
+//    both sides agree, so each thread takes whole 16-byte pieces of code rows.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "launchers.h"
 #include "paged.cuh"
 #include "sm100_primitives.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace fm {
 namespace {
 
-template <int D, int BITS>
-__global__ void __launch_bounds__(128) paged_attention_kernel(PagedAttnParams p) {
-  constexpr int E = D / 32;  // values of a row per lane
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-  if (w >= (int64_t)p.pg.B * p.Nq * p.Hq) return;
-  const int h = (int)(w % p.Hq);
-  const int64_t bi = w / p.Hq;
-  const int i = (int)(bi % p.Nq), b = (int)(bi / p.Nq);
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kMetaInts = 8;
+
+// ---------------------------------------------------------------------------
+// work: groups of items with the same number of tiles, and a CTA's run of units
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int group_batch(const PagedAttnParams& p, int g) { return p.per_head ? g / p.pg.Hkv : g; }
+
+// Keys of sequence b that its rows can see at all, and its first row's position.
+__device__ __forceinline__ int key_bound(const PagedAttnParams& p, int b, int* len_out, int64_t* first) {
   const int len = checked_len(p.pg, p.lens, b);
-  const int64_t pos = (p.start ? (int64_t)p.start[b] : (int64_t)len - p.Nq) + i;
-  const int kvh = h / p.G, hm = p.Hm == 1 ? 0 : h;
-  float q[E], acc[E];
-  const __nv_bfloat16* qp = p.q + b * p.qs[0] + i * p.qs[1] + h * p.qs[2];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(qp[lane * E + e]);
-    acc[e] = 0.f;
+  const int64_t st = p.start ? (int64_t)p.start[b] : (int64_t)len - p.Nq;
+  *len_out = len;
+  *first = st;
+  const int64_t hi = p.causal ? min((int64_t)len, st + p.Nq) : (int64_t)len;
+  return hi > 0 ? (int)hi : 0;
+}
+
+__device__ __forceinline__ int tiles_of(const PagedAttnParams& p, int g) {
+  if (p.counts) return p.counts[g];
+  int len;
+  int64_t st;
+  return (key_bound(p, group_batch(p, g), &len, &st) + p.tile_keys - 1) / p.tile_keys;
+}
+
+// A run of units, walked segment by segment (a segment: tiles [t, t + n) of
+// one item).  Every warp of the CTA walks it the same way.
+struct Walk {
+  int g, in, t, T;   // group, item in the group, first tile, tiles of the group's items
+  int64_t left;      // units left in the run
+  int n;             // tiles of this segment
+  __device__ __forceinline__ void begin(const PagedAttnParams& p) {
+    T = tiles_of(p, g);
+    n = (int)min((int64_t)(T - t), left);
   }
-  float m = -INFINITY, l = 0.f;
-  const int64_t end = p.causal ? min((int64_t)len, pos + 1) : len;
-  for (int j = 0; j < end; ++j) {
-    if (j < p.Nm) {
-      const int64_t at = ((int64_t)b * p.Hm + hm) * p.Nm + j;
-      if (p.lts && p.lts[at] <= pos && pos < p.lte[at]) continue;
-      if (p.uts && p.uts[at] <= pos && pos < p.ute[at]) continue;
+  __device__ __forceinline__ bool next(const PagedAttnParams& p) {
+    left -= n;
+    if (left <= 0) return false;
+    t = 0;
+    if (++in == p.mult) {
+      in = 0;
+      do {
+        ++g;
+        T = tiles_of(p, g);
+      } while (T == 0);
     }
-    const int page = page_of(p.pg, b, j);
-    if (page < 0) continue;
-    const int64_t row = row_of(p.pg, page, kvh, j);
-    float k[E], v[E];
+    n = (int)min((int64_t)T, left);
+    return true;
+  }
+};
+
+struct Item {
+  int b, kvh, row0;
+};
+__device__ __forceinline__ Item item_of(const PagedAttnParams& p, int g, int in, int rows_per_item) {
+  Item it;
+  it.b = group_batch(p, g);
+  const int rb = in % p.n_rb;
+  it.kvh = p.per_head ? g % p.pg.Hkv : in / p.n_rb;
+  it.row0 = rb * rows_per_item;
+  return it;
+}
+
+// ---------------------------------------------------------------------------
+// tiles and shared memory
+// ---------------------------------------------------------------------------
+template <int D, int BITS, int NT>
+struct Cfg {
+  static constexpr int kKT = BITS == 16 && D == 128 ? 32 : 64;  // keys of a tile
+  static constexpr int kRows = 8 * NT;
+  // consumer warps: 8 warps with the loading one leave 255 registers a thread
+  static constexpr int kWarps = NT == 4 ? 4 : NT == 2 ? 7 : 8;
+  static constexpr int kThreads = 32 * kWarps + 32;
+  static constexpr bool kQShared = NT == 4;                     // Q fragments in shared memory
+  static constexpr int kRowBytes = BITS == 16 ? 2 * D : D / 2;
+  static constexpr int kHalf = kKT * kRowBytes;                 // K or V part of a stage
+  static constexpr int kScales = BITS == 4 ? kKT * 4 : 0;
+  static constexpr int kStage = 2 * kHalf + 2 * kScales;
+  static constexpr int kStride = D + 4;                         // floats between rows of the merge buffer
+  static constexpr int kMerge = kWarps * kRows * kStride * 4;
+  static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
+  static constexpr int kPerStage = kStage + kKT * 4 + 16 + 16;  // + words, header, two barriers
+  static constexpr int kFixed = kMerge + kQBytes + 3 * kWarps * kRows * 4 + kRows * 4 + 1024 + 256;
+  static constexpr int kMaxStages = (225 * 1024 - kFixed) / kPerStage;
+  static constexpr int kStages = kMaxStages > 16 ? 16 : kMaxStages;
+  static constexpr int kSmem = kFixed + kStages * kPerStage;
+  static_assert(kStages >= 4, "ring too short");
+};
+
+template <int D, int BITS, int NT>
+struct Smem {
+  using C = Cfg<D, BITS, NT>;
+  uint8_t* stage;      // kStages x kStage, 1024-byte aligned for the swizzle
+  uint32_t* words;     // kStages x kKT row-visibility words
+  int4* hdr;           // kStages: first key, masked, valid boxes
+  uint64_t *full, *empty;
+  float* merge;        // kWarps x kRows x kStride
+  uint2* q;            // Q fragments (kQShared)
+  float *m, *l, *c;    // kWarps x kRows
+  float* qsum;         // kRows
+  long long* scan;     // prologue
+  int* abort;
+  __device__ __forceinline__ explicit Smem(uint8_t* raw) {
+    const uint32_t a = smem_addr(raw);
+    uint8_t* x = raw + ((1024u - (a & 1023u)) & 1023u);
+    stage = x; x += C::kStages * C::kStage;
+    merge = reinterpret_cast<float*>(x); x += C::kMerge;
+    q = reinterpret_cast<uint2*>(x); x += C::kQBytes;
+    words = reinterpret_cast<uint32_t*>(x); x += C::kStages * C::kKT * 4;
+    hdr = reinterpret_cast<int4*>(x); x += C::kStages * 16;
+    full = reinterpret_cast<uint64_t*>(x); x += C::kStages * 8;
+    empty = reinterpret_cast<uint64_t*>(x); x += C::kStages * 8;
+    scan = reinterpret_cast<long long*>(x); x += 16 * 8;
+    m = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
+    l = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
+    c = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
+    qsum = reinterpret_cast<float*>(x); x += C::kRows * 4;
+    abort = reinterpret_cast<int*>(x);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// warp-level building blocks
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// Codes at nibbles i and i + 4 of each half of x as the bf16 pair (code - 8):
+// 0x4300 + code is 128 + code, and 128 + code - 136 is exact.
+__device__ __forceinline__ uint32_t centred(uint32_t x, int i) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(y) : "r"(x >> (4 * i)));  // (x & a) | b
+  asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(0x43084308u));
+  return y;
+}
+
+// Key of slot s (0..7) of an 8-key block in the 4-bit layout: a thread's four
+// keys of V must be spread so that code rows (64 or 32 bytes) meet in few
+// banks, and the rows of K next to one another in a load must have opposite
+// parity.  Any permutation gives the same sums.
+__device__ __forceinline__ int slot_key(int s) { return (s & 1) ? 4 + ((s >> 1) ^ 1) : s >> 1; }
+
+// Largest value over the 8 lanes that share lane % 4.
+__device__ __forceinline__ float max8(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float sum8(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+template <int D, int BITS, int NT>
+__device__ void produce(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
+                        const Smem<D, BITS, NT>& sm, Walk wk, const WaitCtx& wc) {
+  using C = Cfg<D, BITS, NT>;
+  constexpr int KT = C::kKT;
+  const int lane = threadIdx.x & 31;
+  const int box = min(KT, 1 << p.pg.page_shift);  // rows of one copy: part of one page
+  const int boxes = KT / box, box_shift = __ffs(box) - 1;
+  uint32_t n = 0;
+  bool ok = true;
+  do {
+    const Item it = item_of(p, wk.g, wk.in, C::kRows);
+    int len;
+    int64_t first;
+    const int hi = key_bound(p, it.b, &len, &first);
+    // keys that every row of the item sees, without mask vectors
+    const int64_t row_first = first + it.row0 / p.G;
+    const int64_t all = p.causal ? min((int64_t)len, row_first + 1) : (int64_t)len;
+    for (int k0 = 0; k0 < wk.n && ok; k0 += 32) {
+      // 32 tiles at a time: each lane looks up one tile and its pages
+      int j0 = 0, masked = 0, valid = 0, page[4];
+      const int k = k0 + lane;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int x = lane * E + e;
-      if (BITS == 16) {
-        k[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.pg.k)[row * D + x]);
-        v[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.pg.v)[row * D + x]);
-      } else {
-        const uint32_t ks = p.pg.k_scales[row], vs = p.pg.v_scales[row];
-        const int ck = (p.pg.k[row * (D / 2) + x / 2] >> (4 * (x & 1))) & 15;
-        const int cv = (p.pg.v[row * (D / 2) + x / 2] >> (4 * (x & 1))) & 15;
-        k[e] = fmaf(__uint_as_float(ks << 16), (float)ck, __uint_as_float(ks & 0xffff0000u));
-        v[e] = fmaf(__uint_as_float(vs << 16), (float)cv, __uint_as_float(vs & 0xffff0000u));
+      for (int x = 0; x < 4; ++x) page[x] = 0;
+      if (k < wk.n) {
+        const int t = wk.t + k;
+        if (p.list) {
+          const int e = p.list[(int64_t)wk.g * p.list_stride + t];
+          j0 = (e >> 1) * KT;
+          masked = e & 1;
+        } else {
+          j0 = t * KT;
+          masked = (int64_t)j0 + KT > all;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int j = j0 + (x << box_shift);
+          if (x < boxes && j < hi) {
+            page[x] = page_of(p.pg, it.b, j);
+            if (page[x] >= 0) valid |= 1 << x;
+          }
+        }
+        if (valid != (1 << boxes) - 1) masked = 1;
+      }
+      const int m = min(32, wk.n - k0);
+      for (int x = 0; x < m; ++x, ++n) {
+        const int stage = n % C::kStages;
+        const int tj = __shfl_sync(0xffffffffu, j0, x), tm = __shfl_sync(0xffffffffu, masked, x);
+        const int tv_ = __shfl_sync(0xffffffffu, valid, x);
+        const int pg0 = __shfl_sync(0xffffffffu, page[0], x), pg1 = __shfl_sync(0xffffffffu, page[1], x);
+        const int pg2 = __shfl_sync(0xffffffffu, page[2], x), pg3 = __shfl_sync(0xffffffffu, page[3], x);
+        const bool words = p.words_shared && tm;
+        int go = 1;
+        if (lane == 0) {
+          if (n >= (uint32_t)C::kStages)
+            go = mbar_wait(&sm.empty[stage], ((n / C::kStages) & 1u) ^ 1u, wc);
+          if (go) {
+            sm.hdr[stage] = make_int4(tj, tm, tv_, 0);
+            const uint32_t bytes = __popc(tv_) * (2 * box * C::kRowBytes + (BITS == 4 ? 8 * box : 0)) +
+                                   (words ? KT * 4 : 0);
+            mbar_arrive_expect_tx(&sm.full[stage], bytes);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, go, 0);
+        if (!ok) break;
+        // copy c: box c / 4, part c % 4
+        const int bx = lane >> 2, part = lane & 3;
+        uint8_t* st = sm.stage + stage * C::kStage;
+        if (bx < boxes && ((tv_ >> bx) & 1)) {
+          const int pid = bx == 0 ? pg0 : bx == 1 ? pg1 : bx == 2 ? pg2 : pg3;
+          const int64_t row = row_of(p.pg, pid, it.kvh, tj + (bx << box_shift));
+          if (BITS == 16) {
+            if (part < D / 32) {
+              const int half = part & (D / 64 - 1), is_v = part / (D / 64);
+              tma_load_2d(st + is_v * C::kHalf + half * (KT * 128) + (bx << box_shift) * 128, is_v ? tv : tk,
+                          &sm.full[stage], half * 64, (int)row);
+            }
+          } else if (part < 2) {
+            bulk_load(st + part * C::kHalf + (bx << box_shift) * C::kRowBytes,
+                      (part ? p.pg.v : p.pg.k) + row * C::kRowBytes, box * C::kRowBytes, &sm.full[stage]);
+          } else {
+            bulk_load(st + 2 * C::kHalf + (part - 2) * C::kScales + (bx << box_shift) * 4,
+                      (part == 3 ? p.pg.v_scales : p.pg.k_scales) + row, box * 4, &sm.full[stage]);
+          }
+        }
+        if (words && lane == 31)
+          bulk_load(sm.words + stage * KT, p.words + (int64_t)it.b * p.words_stride + tj, KT * 4, &sm.full[stage]);
       }
     }
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s), keep = m == -INFINITY ? 0.f : exp2f(m - mn), pr = exp2f(s - mn);
-    l = l * keep + pr;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(pr, v[e], acc[e] * keep);
-    m = mn;
+  } while (ok && wk.next(p));
+  if (!ok && lane == 0) {  // gave up: let the copies in flight land before the CTA ends
+    WaitCtx w2 = wc;
+    int zero = 0;
+    w2.abort = &zero;
+    const uint32_t from = n > (uint32_t)C::kStages ? n - C::kStages : 0u;
+    for (uint32_t i = from; i < n; ++i) mbar_wait(&sm.full[i % C::kStages], (i / C::kStages) & 1u, w2);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+}
+
+template <int D, int BITS, int NT>
+__device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, Walk wk, const WaitCtx& wc) {
+  using C = Cfg<D, BITS, NT>;
+  constexpr int KT = C::kKT, MT = D / 16, KS = D / 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g8 = lane >> 2, q4 = lane & 3;  // the fragment's row in a block of 8, and its column pair
+  const int box_shift = min(p.pg.page_shift, KT == 32 ? 5 : 6);
+  uint32_t base = 0;
+  bool alive = true, first_seg = true;
+  do {
+    const Item it = item_of(p, wk.g, wk.in, C::kRows);
+    int len;
+    int64_t first;
+    key_bound(p, it.b, &len, &first);
+    const int R = p.Nq * p.G - it.row0;  // real rows of the block (may exceed kRows)
+    const __nv_bfloat16* qb = p.q + it.b * p.qs[0];
+
+    // ---- Q fragments (B operand of S^T: k = values of the head, n = rows) ----
+    uint2 qf[C::kQShared ? 1 : KS][C::kQShared ? 1 : NT];
+    float qsum[2 * NT];
+    auto load_q = [&](int ks, int nt) {
+      const int r = nt * 8 + g8;
+      if (r >= R) return make_uint2(0u, 0u);
+      const int row = it.row0 + r, i = row / p.G, h = it.kvh * p.G + row % p.G;
+      const __nv_bfloat16* src = qb + i * p.qs[1] + h * p.qs[2];
+      if (BITS == 16) {
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * q4);
+        return make_uint2(s[0], s[4]);
+      } else {
+        // values base + {0, 4} and base + {1, 5}: the nibble pairs that centred() gives
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(src + (D / 4) * q4 + 8 * (ks >> 1) + 2 * (ks & 1));
+        const uint32_t lo = s[0], hi = s[2];
+        return make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+      }
+    };
+    if (!C::kQShared) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) p.o[w * D + lane * E + e] = __float2bfloat16(acc[e] * inv);
-  if (lane == 0)
-    p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt] = load_q(ks, nt);
+      if (BITS == 4) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float s = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const uint2 u = qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
+            s += (__uint_as_float(u.x << 16) + __uint_as_float(u.x & 0xffff0000u)) +
+                 (__uint_as_float(u.y << 16) + __uint_as_float(u.y & 0xffff0000u));
+          }
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);  // lanes of row g8 hold its sum
+          qsum[2 * nt] = __shfl_sync(0xffffffffu, s, 8 * q4);
+          qsum[2 * nt + 1] = __shfl_sync(0xffffffffu, s, 8 * q4 + 4);
+        }
+      }
+    } else {
+      for (int x = warp; x < KS * NT; x += C::kWarps) sm.q[x * 32 + lane] = load_q(x / NT, x % NT);
+      if (BITS == 4 && warp == 0) {
+        float s = 0.f;
+        if (lane < C::kRows && lane < R) {
+          const int row = it.row0 + lane, i = row / p.G, h = it.kvh * p.G + row % p.G;
+          const __nv_bfloat16* src = qb + i * p.qs[1] + h * p.qs[2];
+          for (int x = 0; x < D; ++x) s += __bfloat162float(src[x]);
+        }
+        if (lane < C::kRows) sm.qsum[lane] = s;
+      }
+      named_barrier_sync(1, 32 * C::kWarps);
+      if (BITS == 4) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          qsum[2 * nt] = sm.qsum[nt * 8 + 2 * q4];
+          qsum[2 * nt + 1] = sm.qsum[nt * 8 + 2 * q4 + 1];
+        }
+      }
+    }
+
+    float acc[MT][NT][4], mx[2 * NT], sum[2 * NT], cor[2 * NT];
+#pragma unroll
+    for (int x = 0; x < 2 * NT; ++x) {
+      mx[x] = -INFINITY;
+      sum[x] = 0.f;
+      cor[x] = 0.f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
+
+    const uint32_t end = base + wk.n;
+    for (uint32_t n = base + ((uint32_t)warp + C::kWarps - base % C::kWarps) % C::kWarps; n < end; n += C::kWarps) {
+      const int stage = n % C::kStages;
+      if (alive) alive = mbar_wait(&sm.full[stage], (n / C::kStages) & 1u, wc);
+      alive = __all_sync(0xffffffffu, alive);
+      if (!alive) continue;  // keeps walking: the barriers at the ends of segments are still met
+      const int4 hd = sm.hdr[stage];
+      uint8_t* st = sm.stage + stage * C::kStage;
+      const uint32_t kaddr = smem_addr(st), vaddr = kaddr + C::kHalf;
+      bool wrote = false;
+#pragma unroll 1
+      for (int sb = 0; sb < KT; sb += 32) {
+        // ---- S^T: 32 keys x rows ----
+        float s[2][NT][4];
+#pragma unroll
+        for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[m2][nt][e] = 0.f;
+        if (BITS == 16) {
+          const int key = sb + (lane & 7) + ((lane >> 3) & 1) * 8, hi = lane >> 4;
+#pragma unroll
+          for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              const int kk = key + m2 * 16, ch = ks * 2 + hi;
+              uint32_t a[4];
+              ldsm4(a, kaddr + (ch >> 3) * (KT * 128) + kk * 128 + (((ch & 7) ^ (kk & 7)) << 4));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint2 b = C::kQShared ? sm.q[(ks * NT + nt) * 32 + lane] : qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
+                mma16816(s[m2][nt], a, b.x, b.y);
+              }
+            }
+        } else {
+#pragma unroll
+          for (int m2 = 0; m2 < 2; ++m2) {
+            uint32_t r0[D / 32], r1[D / 32];  // the thread's piece of two code rows
+            const uint8_t* row = st + (sb + m2 * 16 + slot_key(g8)) * C::kRowBytes + q4 * (D / 8);
+            if (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(row), y = *reinterpret_cast<const uint4*>(row + 8 * C::kRowBytes);
+              r0[0] = x.x; r0[1] = x.y; r0[D / 32 - 2] = x.z; r0[D / 32 - 1] = x.w;
+              r1[0] = y.x; r1[1] = y.y; r1[D / 32 - 2] = y.z; r1[D / 32 - 1] = y.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(row), y = *reinterpret_cast<const uint2*>(row + 8 * C::kRowBytes);
+              r0[0] = x.x; r0[1] = x.y;
+              r1[0] = y.x; r1[1] = y.y;
+            }
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              const int i = 2 * (ks & 1);
+              const uint32_t a[4] = {centred(r0[ks >> 1], i), centred(r1[ks >> 1], i), centred(r0[ks >> 1], i + 1),
+                                     centred(r1[ks >> 1], i + 1)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint2 b = C::kQShared ? sm.q[(ks * NT + nt) * 32 + lane] : qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
+                mma16816(s[m2][nt], a, b.x, b.y);
+              }
+            }
+          }
+        }
+        // keys of the thread's four fragment rows
+        auto key_of = [&](int m2, int hf) { return sb + m2 * 16 + hf * 8 + (BITS == 4 ? slot_key(g8) : g8); };
+        float vs[2][2], vm[2][2];
+        if (BITS == 4) {
+          const uint32_t* ksc = reinterpret_cast<const uint32_t*>(st + 2 * C::kHalf);
+          const uint32_t* vsc = ksc + KT;
+#pragma unroll
+          for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int key = key_of(m2, hf);
+              const uint32_t a = ksc[key], b = vsc[key];
+              const float ks_ = __uint_as_float(a << 16), km = fmaf(8.f, ks_, __uint_as_float(a & 0xffff0000u));
+              vs[m2][hf] = __uint_as_float(b << 16);
+              vm[m2][hf] = fmaf(8.f, vs[m2][hf], __uint_as_float(b & 0xffff0000u));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  s[m2][nt][2 * hf + e] = fmaf(ks_, s[m2][nt][2 * hf + e], km * qsum[2 * nt + e]);
+            }
+        }
+        // ---- hidden pairs ----
+        const bool masked = hd.y != 0;
+        uint32_t hid = 0;  // bit (m2 * 2 + hf) * 2 NT + nt * 2 + e
+        if (masked) {
+#pragma unroll
+          for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int key = key_of(m2, hf), j = hd.x + key;
+              const bool there = (hd.z >> (key >> box_shift)) & 1;
+              const uint32_t w = p.words_shared ? sm.words[stage * KT + key] : 0u;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int row = it.row0 + nt * 8 + 2 * q4 + e, i = row / p.G;
+                  bool see;
+                  if (p.words_shared) {
+                    see = (w >> (i & 31)) & 1u;
+                  } else if (p.words) {
+                    see = false;
+                    if (i < p.Nq && there) {
+                      const int hm = p.Hm == 1 ? 0 : it.kvh * p.G + row % p.G;
+                      const int64_t at = ((int64_t)(it.b * p.Hm + hm) * p.n_words + (i >> 5)) * p.words_stride + j;
+                      see = (p.words[at] >> (i & 31)) & 1u;
+                    }
+                  } else {
+                    see = j < len && (!p.causal || j <= first + i);
+                  }
+                  if (!(see && there)) {
+                    hid |= 1u << ((m2 * 2 + hf) * 2 * NT + nt * 2 + e);
+                    s[m2][nt][2 * hf + e] = -INFINITY;
+                  }
+                }
+            }
+        }
+        // ---- running maximum ----
+        float mn[2 * NT];
+        bool grew = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
+            mn[2 * nt + e] = fmaxf(mx[2 * nt + e], max8(x));
+            grew |= mn[2 * nt + e] > mx[2 * nt + e];
+          }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int x = 0; x < 2 * NT; ++x) {
+            const float f = mx[x] == -INFINITY ? 0.f : fast_exp2((mx[x] - mn[x]) * p.scale_log2);
+            mx[x] = mn[x];
+            sum[x] *= f;
+            cor[x] *= f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              acc[mt][x >> 1][x & 1] *= f;
+              acc[mt][x >> 1][2 + (x & 1)] *= f;
+            }
+          }
+        }
+        // ---- P^T, its sums, and its transpose as the B operand of O^T ----
+        float off[2 * NT];
+#pragma unroll
+        for (int x = 0; x < 2 * NT; ++x) off[x] = mx[x] == -INFINITY ? 0.f : mx[x] * p.scale_log2;
+        uint32_t pb[2][NT][2];
+#pragma unroll
+        for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float w[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int x = 2 * nt + e;
+                const float pr = fast_exp2(fmaf(s[m2][nt][2 * hf + e], p.scale_log2, -off[x]));
+                sum[x] += pr;
+                w[e] = pr;
+                if (BITS == 4) {
+                  // a hidden key's scale may be anything, NaN included
+                  const bool hidden = (hid >> ((m2 * 2 + hf) * 2 * NT + x)) & 1u;
+                  w[e] = hidden ? 0.f : pr * vs[m2][hf];
+                  cor[x] = hidden ? cor[x] : fmaf(pr, vm[m2][hf], cor[x]);
+                } else {
+                  s[m2][nt][2 * hf + e] = pr;
+                }
+              }
+              pb[m2][nt][hf] = transpose8x8(pack_bf16x2(w[0], w[1]));
+            }
+        // ---- values that are not finite, in a tile that some row does not see whole ----
+        // 0 * NaN must not reach a row that the key is hidden from: such keys leave the product and are
+        // added by rows that see them, one by one.
+        if (BITS == 16 && masked) {
+          const int kk = sb + lane;
+          __nv_bfloat162 z = __float2bfloat162_rn(0.f);
+          const __nv_bfloat162 zero = z;
+#pragma unroll
+          for (int ch = 0; ch < D / 8; ++ch) {
+            const uint4 u = *reinterpret_cast<const uint4*>(st + C::kHalf + (ch >> 3) * (KT * 128) + kk * 128 + (((ch & 7) ^ (kk & 7)) << 4));
+            const uint32_t ww[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&ww[y]), zero, z);
+          }
+          const float2 zf = __bfloat1622float2(z);
+          uint32_t bad = __ballot_sync(0xffffffffu, !(zf.x == 0.f && zf.y == 0.f));
+          while (bad) {
+            const int k5 = __ffs(bad) - 1;  // key in the 32
+            bad &= bad - 1;
+            const int src = (k5 & 7) * 4 + q4, sel = k5 >> 3;  // sel = m2 * 2 + hf
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float c0 = sel & 2 ? s[1][nt][e] : s[0][nt][e], c1 = sel & 2 ? s[1][nt][2 + e] : s[0][nt][2 + e];
+                const float pr = __shfl_sync(0xffffffffu, sel & 1 ? c1 : c0, src);
+                const uint32_t hb = __shfl_sync(0xffffffffu, hid, src);
+                if (!((hb >> (sel * 2 * NT + nt * 2 + e)) & 1u)) {
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                      const int x = mt * 16 + u * 8 + g8, ch = x >> 3, k6 = sb + k5;
+                      const __nv_bfloat16 v = *reinterpret_cast<const __nv_bfloat16*>(
+                          st + C::kHalf + (ch >> 3) * (KT * 128) + k6 * 128 + (((ch & 7) ^ (k6 & 7)) << 4) + (x & 7) * 2);
+                      acc[mt][nt][2 * u + e] = fmaf(pr, __bfloat162float(v), acc[mt][nt][2 * u + e]);
+                    }
+                }
+              }
+            __syncwarp();
+            if (lane < D / 8)
+              *reinterpret_cast<uint4*>(st + C::kHalf + (lane >> 3) * (KT * 128) + (sb + k5) * 128 + ((lane & 7) << 4)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            wrote = true;
+          }
+          __syncwarp();
+        }
+        // ---- O^T += V^T P^T ----
+        if (BITS == 16) {
+          const int key = sb + (lane & 7) + (lane >> 4) * 8, hi = (lane >> 3) & 1;
+#pragma unroll
+          for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const int kk = key + m2 * 16, ch = mt * 2 + hi;
+              uint32_t a[4];
+              ldsm4_t(a, vaddr + (ch >> 3) * (KT * 128) + kk * 128 + (((ch & 7) ^ (kk & 7)) << 4));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(acc[mt][nt], a, pb[m2][nt][0], pb[m2][nt][1]);
+            }
+        } else {
+#pragma unroll
+          for (int m2 = 0; m2 < 2; ++m2) {
+            // slots 2 q4, 2 q4 + 1 and the same + 8; the thread takes values [g8 D/8, (g8 + 1) D/8) of each
+            uint32_t r[4][D / 64];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int key = sb + m2 * 16 + (y >> 1) * 8 + slot_key(2 * q4 + (y & 1));
+              const uint8_t* src = st + C::kHalf + key * C::kRowBytes + g8 * (D / 16);
+              if (D == 128) {
+                const uint2 x = *reinterpret_cast<const uint2*>(src);
+                r[y][0] = x.x;
+                r[y][D / 64 - 1] = x.y;
+              } else {
+                r[y][0] = *reinterpret_cast<const uint32_t*>(src);
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w)
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {  // low and high 16 bits: four values each
+                const uint32_t lo = __byte_perm(r[0][w], r[1][w], hh ? 0x7632 : 0x5410);
+                const uint32_t up = __byte_perm(r[2][w], r[3][w], hh ? 0x7632 : 0x5410);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int mt = w * 4 + hh * 2 + z;
+                  const uint32_t a[4] = {centred(lo, 2 * z), centred(lo, 2 * z + 1), centred(up, 2 * z),
+                                         centred(up, 2 * z + 1)};
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma16816(acc[mt][nt], a, pb[m2][nt][0], pb[m2][nt][1]);
+                }
+              }
+          }
+        }
+      }
+      if (wrote) fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[stage]);
+    }
+    base = end;
+
+    // ---- the warps' sums together ----
+#pragma unroll
+    for (int x = 0; x < 2 * NT; ++x) {
+      sum[x] = sum8(sum[x]);
+      if (BITS == 4) cor[x] = sum8(cor[x]);
+    }
+    if (g8 == 0) {
+#pragma unroll
+      for (int x = 0; x < 2 * NT; ++x) {
+        const int r = warp * C::kRows + (x >> 1) * 8 + 2 * q4 + (x & 1);
+        sm.m[r] = mx[x];
+        sm.l[r] = sum[x];
+        if (BITS == 4) sm.c[r] = cor[x];
+      }
+    }
+    named_barrier_sync(1, 32 * C::kWarps);
+#pragma unroll
+    for (int x = 0; x < 2 * NT; ++x) {
+      const int r = (x >> 1) * 8 + 2 * q4 + (x & 1);
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, sm.m[w * C::kRows + r]);
+      const float f = mx[x] == -INFINITY ? 0.f : fast_exp2((mx[x] - top) * p.scale_log2);
+      float* dst = sm.merge + (warp * C::kRows + r) * C::kStride;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (BITS == 16) {
+          dst[mt * 16 + g8] = acc[mt][x >> 1][x & 1] * f;
+          dst[mt * 16 + 8 + g8] = acc[mt][x >> 1][2 + (x & 1)] * f;
+        } else {
+          *reinterpret_cast<float2*>(dst + g8 * (D / 8) + 2 * mt) =
+              make_float2(acc[mt][x >> 1][x & 1] * f, acc[mt][x >> 1][2 + (x & 1)] * f);
+        }
+      }
+    }
+    named_barrier_sync(1, 32 * C::kWarps);
+    const bool whole = wk.n == wk.T;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1);
+    for (int x = threadIdx.x; x < C::kRows * (D / 4); x += 32 * C::kWarps) {
+      const int r = x / (D / 4), d4 = x % (D / 4);
+      if (r >= R) continue;
+      float top = -INFINITY, L = 0.f, cc = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, sm.m[w * C::kRows + r]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < C::kWarps; ++w) {
+        const float m = sm.m[w * C::kRows + r];
+        const float f = m == -INFINITY ? 0.f : fast_exp2((m - top) * p.scale_log2);
+        L = fmaf(sm.l[w * C::kRows + r], f, L);
+        if (BITS == 4) cc = fmaf(sm.c[w * C::kRows + r], f, cc);
+        const float4 v = *reinterpret_cast<const float4*>(sm.merge + (w * C::kRows + r) * C::kStride + 4 * d4);
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+      if (BITS == 4) {
+        o.x += cc;
+        o.y += cc;
+        o.z += cc;
+        o.w += cc;
+      }
+      if (whole) {
+        const int row = it.row0 + r, i = row / p.G, h = it.kvh * p.G + row % p.G;
+        const float inv = top == -INFINITY ? 0.f : 1.f / L;
+        const int64_t at = (((int64_t)it.b * p.Nq + i) * p.Hq + h) * D + 4 * d4;
+        *reinterpret_cast<uint2*>(p.o + at) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (d4 == 0)
+          p.lse[((int64_t)it.b * p.Hq + h) * p.Nq + i] =
+              top == -INFINITY ? -INFINITY : fmaf(top, p.scale_log2, log2f(L)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(p.part + (slot * C::kRows + r) * D + 4 * d4) = o;
+        if (d4 == 0) p.stat[slot * C::kRows + r] = make_float2(top, L);
+      }
+    }
+    named_barrier_sync(1, 32 * C::kWarps);
+    first_seg = false;
+  } while (wk.next(p));
+}
+
+template <int D, int BITS, int NT>
+__global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                           const __grid_constant__ PagedAttnParams p) {
+  using C = Cfg<D, BITS, NT>;
+  extern __shared__ uint8_t raw[];
+  Smem<D, BITS, NT> sm(raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    *sm.abort = 0;
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    fence_mbar_init();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- this CTA's run of units: total, then the group it begins in ----
+  const int per = (p.n_groups + C::kThreads - 1) / C::kThreads;
+  const int ga = min(tid * per, p.n_groups), gb = min(ga + per, p.n_groups);
+  long long mine = 0;
+  for (int g = ga; g < gb; ++g) mine += tiles_of(p, g);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) sm.scan[warp] = incl;
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w <= C::kWarps; ++w) {
+    if (w < warp) before += sm.scan[w];
+    total += sm.scan[w];
+  }
+  before += incl - mine;
+  total *= p.mult;
+  before *= p.mult;
+  const long long want = (total + p.min_tiles - 1) / p.min_tiles;
+  const long long ctas = want < gridDim.x ? (want > 0 ? want : 1) : gridDim.x;
+  const bool works = blockIdx.x < ctas && total > 0;
+  const long long u0 = works ? blockIdx.x * total / ctas : 0, u1 = works ? (blockIdx.x + 1) * total / ctas : 0;
+  if (u1 > u0 && mine > 0 && u0 >= before && u0 < before + mine * p.mult) {
+    long long at = before;
+    int g = ga, T = tiles_of(p, g);
+    while (u0 >= at + (long long)T * p.mult) {
+      at += (long long)T * p.mult;
+      T = tiles_of(p, ++g);
+    }
+    sm.scan[12] = g;
+    sm.scan[13] = u0 - at;
+  }
+  __syncthreads();
+
+  // rows of sequences with no visible tile
+  for (int g = blockIdx.x; g < p.n_groups; g += gridDim.x) {
+    if (tiles_of(p, g) != 0) continue;
+    const int b = group_batch(p, g), heads = p.per_head ? p.G : p.Hq, h0 = p.per_head ? (g % p.pg.Hkv) * p.G : 0;
+    for (int64_t x = tid; x < (int64_t)p.Nq * heads * (D / 8); x += C::kThreads) {
+      const int c = (int)(x % (D / 8)), h = h0 + (int)(x / (D / 8) % heads), i = (int)(x / (D / 8) / heads);
+      *reinterpret_cast<uint4*>(p.o + (((int64_t)b * p.Nq + i) * p.Hq + h) * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+      if (c == 0) p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] = -INFINITY;
+    }
+  }
+  if (u1 <= u0) {
+    if (tid == 0) p.meta[blockIdx.x * kMetaInts] = -1;
+    return;
+  }
+
+  Walk wk;
+  wk.g = (int)sm.scan[12];
+  const long long off = sm.scan[13];
+  wk.T = tiles_of(p, wk.g);
+  wk.in = (int)(off / wk.T);
+  wk.t = (int)(off % wk.T);
+  wk.left = u1 - u0;
+  wk.n = (int)min((long long)(wk.T - wk.t), (long long)wk.left);
+
+  WaitCtx wc;
+  wc.abort = sm.abort;
+  wc.status = p.pg.status;
+  wc.limit_ns = p.wait_limit_ns;
+  wc.smem_base = smem_addr(raw);
+  wc.kernel = 5;
+  if (warp == C::kWarps) {
+    // an item that begins in this run and goes on in the next ones: where its parts are
+    if (lane == 0) {
+      int* meta = p.meta + blockIdx.x * kMetaInts;
+      Walk w = wk;
+      bool first = true;
+      long long u = u0;
+      while (u + w.n < u1) {
+        u += w.n;
+        first = false;
+        w.next(p);
+      }
+      if (w.t == 0 && w.n < w.T) {
+        const Item it = item_of(p, w.g, w.in, C::kRows);
+        const long long last = u + w.T - 1;
+        meta[0] = it.b;
+        meta[1] = it.kvh;
+        meta[2] = it.row0;
+        meta[3] = (int)(((last + 1) * ctas + total - 1) / total - 1);  // the CTA that ends it
+        meta[4] = first ? 0 : 1;
+      } else {
+        meta[0] = -1;
+      }
+    }
+    __syncwarp();
+    produce<D, BITS, NT>(p, &tk, &tv, sm, wk, wc);
+  } else {
+    consume<D, BITS, NT>(p, sm, wk, wc);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// joining the parts of cut items: one CTA per (run, row)
+// ---------------------------------------------------------------------------
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
+  constexpr int LG = D / 4, NGR = 256 / LG;
+  __shared__ float w[256], red[8];
+  __shared__ float4 buf[NGR][LG];
+  griddep_wait();
+  const int* meta = p.meta + blockIdx.x * kMetaInts;
+  const int b = meta[0];
+  if (b < 0) return;
+  const int r = blockIdx.y, row = meta[2] + r;
+  if (row >= p.Nq * p.G) return;
+  const int kvh = meta[1], parts = meta[3] - (int)blockIdx.x + 1, tid = threadIdx.x;
+  auto slot = [&](int k) { return 2 * ((int64_t)blockIdx.x + k) + (k == 0 ? meta[4] : 0); };
+  // weights of the parts (at most 160)
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (tid < parts) ml = p.stat[slot(tid) * ROWS + r];
+  float top = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) == 0) red[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, red[i]);
+  const float f = ml.x == -INFINITY ? 0.f : fast_exp2((ml.x - top) * p.scale_log2);
+  w[tid] = f;
+  float L = ml.y * f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  __syncthreads();
+  if ((tid & 31) == 0) red[tid >> 5] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) L += red[i];
+  const int grp = tid / LG, d4 = tid % LG;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = grp; k < parts; k += NGR) {
+    const float4 v = *reinterpret_cast<const float4*>(p.part + (slot(k) * ROWS + r) * D + 4 * d4);
+    const float wk = w[k];
+    if (wk == 0.f) continue;  // a part that saw nothing
+    o.x = fmaf(wk, v.x, o.x);
+    o.y = fmaf(wk, v.y, o.y);
+    o.z = fmaf(wk, v.z, o.z);
+    o.w = fmaf(wk, v.w, o.w);
+  }
+  buf[grp][d4] = o;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int k = 1; k < NGR; ++k) {
+    const float4 v = buf[k][d4];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
+  }
+  const int i = row / p.G, h = kvh * p.G + row % p.G;
+  const float inv = top == -INFINITY ? 0.f : 1.f / L;
+  *reinterpret_cast<uint2*>(p.o + (((int64_t)b * p.Nq + i) * p.Hq + h) * D + 4 * d4) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (d4 == 0)
+    p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] =
+        top == -INFINITY ? -INFINITY : fmaf(top, p.scale_log2, log2f(L)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// plan: row-visibility words and the list of visible tiles (one cluster of 8
+// CTAs per group)
+// ---------------------------------------------------------------------------
+constexpr int kPlanCtas = 8, kPlanThreads = 256, kPlanTiles = 2048;  // tiles of one CTA at a time
+
+// Rows [p0, p0 + 32) with [lo, hi) cut out, as a word.
+__device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t p0) {
+  const int a = (int)min(max(lo - p0, (int64_t)0), (int64_t)32), b = (int)min(max(hi - p0, (int64_t)0), (int64_t)32);
+  return bit_range(a, b);
+}
+
+template <int KT>
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    paged_plan_kernel(const __grid_constant__ PagedAttnParams p, int* counts, int* list, uint32_t* words) {
+  __shared__ uint8_t flag[kPlanTiles];
+  __shared__ int cnt, wsum[kPlanThreads / 32];
+  griddep_launch_dependents();
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank(), g = blockIdx.x / kPlanCtas;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = group_batch(p, g);
+  const int hm0 = p.per_head ? (g % p.pg.Hkv) * p.G : 0, nh = p.per_head ? p.G : 1;
+  int len;
+  int64_t first;
+  const int hi = key_bound(p, b, &len, &first);
+  const int tiles = (hi + KT - 1) / KT;
+  int done = 0;
+  for (int t0 = 0; t0 < tiles; t0 += kPlanCtas * kPlanTiles) {
+    const int block = min(tiles - t0, kPlanCtas * kPlanTiles);
+    const int share = (block + kPlanCtas - 1) / kPlanCtas;
+    const int a = min(rank * share, block), n = min(share, block - a);  // this CTA's tiles: t0 + a + [0, n)
+    int seen = 0;
+    for (int t = warp; t < n; t += kPlanThreads / 32) {
+      const int j0 = (t0 + a + t) * KT;
+      bool any = false, all = true;
+#pragma unroll
+      for (int jj = 0; jj < KT; jj += 32) {
+        const int j = j0 + jj + lane;
+        for (int h = 0; h < nh; ++h) {
+          const int64_t at = ((int64_t)b * p.Hm + hm0 + h);
+          int lts = 0, lte = 0, uts = 0, ute = 0;
+          if (j < p.Nm && j < hi) {
+            const int64_t m = at * p.Nm + j;
+            if (p.lts) {
+              lts = p.lts[m];
+              lte = p.lte[m];
+            }
+            if (p.uts) {
+              uts = p.uts[m];
+              ute = p.ute[m];
+            }
+          }
+          for (int w = 0; w < p.n_words; ++w) {
+            const int64_t p0 = first + 32 * w;
+            const uint32_t rows = bit_range(0, min(32, p.Nq - 32 * w));
+            uint32_t see = 0;
+            if (j < hi) {
+              uint32_t hid = rows_in(lts, lte, p0) | rows_in(uts, ute, p0);
+              if (p.causal) hid |= rows_in(p0, j, p0);
+              see = rows & ~hid;
+            }
+            words[(at * p.n_words + w) * p.words_stride + j] = see;
+            any |= see != 0;
+            all &= see == rows;
+          }
+        }
+      }
+      any = __any_sync(0xffffffffu, any);
+      all = __all_sync(0xffffffffu, all);
+      if (lane == 0) flag[t] = any ? (all ? 2 : 1) : 0;
+      seen += any;
+    }
+    if (lane == 0) wsum[warp] = seen;
+    __syncthreads();
+    if (tid == 0) {
+      int s = 0;
+      for (int i = 0; i < kPlanThreads / 32; ++i) s += wsum[i];
+      cnt = s;
+    }
+    cl.sync();
+    int at = done, total = 0;
+    for (int r = 0; r < kPlanCtas; ++r) {
+      const int c = *cl.map_shared_rank(&cnt, r);
+      if (r < rank) at += c;
+      total += c;
+    }
+    // this CTA's visible tiles in order
+    const int each = (n + kPlanThreads - 1) / kPlanThreads, ta = min(tid * each, n), tb = min(ta + each, n);
+    int mine = 0;
+    for (int t = ta; t < tb; ++t) mine += flag[t] != 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) at += wsum[i];
+    at += incl - mine;
+    for (int t = ta; t < tb; ++t)
+      if (flag[t]) list[(int64_t)g * p.list_stride + at++] = ((t0 + a + t) << 1) | (flag[t] == 1);
+    done += total;
+    cl.sync();  // every CTA has read the counts, and this one's flags and sums are free again
+  }
+  if (rank == 0 && tid == 0) counts[g] = done;
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st) {
-  const int64_t warps = (int64_t)p.pg.B * p.Nq * p.Hq;
-  if (warps == 0) return cudaSuccess;
-  const unsigned blocks = (unsigned)((warps + 3) / 4);
-  note_launch();
-  if (p.pg.d == 128) {
-    if (p.pg.bits == 4) paged_attention_kernel<128, 4><<<blocks, 128, 0, st>>>(p);
-    else paged_attention_kernel<128, 16><<<blocks, 128, 0, st>>>(p);
+template <int D, int BITS, int NT>
+static cudaError_t launch_variant(const PagedAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                                  cudaStream_t st) {
+  using C = Cfg<D, BITS, NT>;
+  auto* k = paged_attention_kernel<D, BITS, NT>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(k), C::kSmem);
+  if (e != cudaSuccess) return e;
+  if (p.list) {
+    e = launch_after(k, dim3(grid), dim3(C::kThreads), C::kSmem, st, tk, tv, p);
   } else {
-    if (p.pg.bits == 4) paged_attention_kernel<64, 4><<<blocks, 128, 0, st>>>(p);
-    else paged_attention_kernel<64, 16><<<blocks, 128, 0, st>>>(p);
+    note_launch();
+    k<<<grid, C::kThreads, C::kSmem, st>>>(tk, tv, p);
+    e = cudaGetLastError();
   }
-  return cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(paged_merge_kernel<D, C::kRows>, dim3(grid, C::kRows), dim3(256), 0, st, p);
+}
+
+int paged_tile_keys(int d, int bits) { return bits == 16 && d == 128 ? 32 : 64; }
+
+cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                                   int* counts, int* list, uint32_t* words, cudaStream_t st) {
+  if (p.list) {
+    note_launch();
+    const unsigned blocks = (unsigned)p.n_groups * kPlanCtas;
+    if (p.tile_keys == 32) paged_plan_kernel<32><<<blocks, kPlanThreads, 0, st>>>(p, counts, list, words);
+    else paged_plan_kernel<64><<<blocks, kPlanThreads, 0, st>>>(p, counts, list, words);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+#define FM_PAGED(D, BITS)                                                              \
+  if (p.pg.d == D && p.pg.bits == BITS) {                                              \
+    if (p.rows == 8) return launch_variant<D, BITS, 1>(p, tk, tv, grid, st);           \
+    if (p.rows == 16) return launch_variant<D, BITS, 2>(p, tk, tv, grid, st);          \
+    return launch_variant<D, BITS, 4>(p, tk, tv, grid, st);                            \
+  }
+  FM_PAGED(64, 16)
+  FM_PAGED(128, 16)
+  FM_PAGED(64, 4)
+  FM_PAGED(128, 4)
+#undef FM_PAGED
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace fm

@@ -397,7 +397,7 @@ int flashmask_get_status(void);
  * the bounded wait that caused the first FLASHMASK_ERR_TIMEOUT since the
  * status word was last cleared (left unchanged when none occurred since):
  * info[0] kernel (0 forward, 1 backward key side, 2 backward query side,
- * 3 the flashmask_test_wait_timeout self-test, 4 fused backward), info[1] byte offset of the
+ * 3 the flashmask_test_wait_timeout self-test, 4 fused backward, 5 paged attention), info[1] byte offset of the
  * mbarrier in that kernel's shared-memory block, info[2] the phase parity
  * waited for, info[3] block index, info[4] thread index.  Returns
  * FLASHMASK_ERR_INVALID_ARG for a NULL info. */
