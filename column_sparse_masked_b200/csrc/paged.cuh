@@ -59,12 +59,21 @@ struct PagedAttnParams {
   const uint32_t* words;    // [B, Hm, n_words, words_stride]: bit i = row 32 w + i sees the key
   int n_words;
   int64_t words_stride;
-  int words_shared;         // one word per key serves all rows: loaded with the tile
+  int words_shared;         // one word per key serves all rows
   // partial sums of cut items: two slots per CTA
   float* part;              // [2 grid, rows, d]
   float2* stat;             // [2 grid, rows]: running maximum, sum
   int* meta;                // [grid, 8]: the item that begins in a CTA's run and goes on in the next
   uint64_t wait_limit_ns;
+};
+
+// What the plan kernels write: counts, list and words as above, and the class of every tile
+// (0 no pair visible, 1 some pair hidden, 2 all visible), [n_groups, list_stride].
+struct PlanOut {
+  int *counts, *list;
+  uint32_t* words;
+  uint8_t* flags;
+  int chunks;  // plan CTAs per group
 };
 
 constexpr int kPagedMaxCtas = 160;
@@ -95,8 +104,8 @@ __device__ __forceinline__ int checked_len(const Pages& pg, const int32_t* lens,
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st);
 cudaError_t launch_paged_gather(const GatherParams& p, cudaStream_t st);
 int paged_tile_keys(int d, int bits);
-// Plan (when p.list is set; counts, list and words are its writable views), attention and merge.
+// Plan (when p.list is set), attention and merge.
 cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                                   int* counts, int* list, uint32_t* words, cudaStream_t st);
+                                   PlanOut plan, cudaStream_t st);
 
 }  // namespace fm

@@ -79,7 +79,7 @@ int check_paged_rows(const flashmask_pages* pg, const flashmask_paged_rows* r) {
 struct PagedLayout {
   int per_head, n_groups, mult, n_rb, rows, tile_keys, n_words;
   int64_t keys;  // capacity of the table, in whole tiles
-  size_t part, stat, meta, counts, list, words, bytes;
+  size_t part, stat, meta, counts, list, words, flags, bytes;
 };
 
 PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& r) {
@@ -104,6 +104,7 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
     L.counts = take((size_t)L.n_groups * 4);
     L.list = take((size_t)L.n_groups * (L.keys / L.tile_keys) * 4);
     L.words = take((size_t)pg.B * r.Hm * L.n_words * L.keys * 4);
+    L.flags = take((size_t)L.n_groups * (L.keys / L.tile_keys));
   }
   L.bytes = off;
   return L;
@@ -228,12 +229,12 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
   p.part = reinterpret_cast<float*>(ws + L.part);
   p.stat = reinterpret_cast<float2*>(ws + L.stat);
   p.meta = reinterpret_cast<int*>(ws + L.meta);
-  int *counts = nullptr, *list = nullptr;
-  uint32_t* words = nullptr;
+  PlanOut plan{};
   if (masked) {
-    p.counts = counts = reinterpret_cast<int*>(ws + L.counts);
-    p.list = list = reinterpret_cast<int*>(ws + L.list);
-    p.words = words = reinterpret_cast<uint32_t*>(ws + L.words);
+    p.counts = plan.counts = reinterpret_cast<int*>(ws + L.counts);
+    p.list = plan.list = reinterpret_cast<int*>(ws + L.list);
+    p.words = plan.words = reinterpret_cast<uint32_t*>(ws + L.words);
+    plan.flags = ws + L.flags;
     p.list_stride = (int)(L.keys / L.tile_keys);
     p.n_words = L.n_words;
     p.words_stride = L.keys;
@@ -248,7 +249,7 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
     FM_TRY(make_rows_map(&tv, pages->v, rows, pages->d, box));
   }
   const int grid = persistent_grid(kPagedMaxCtas, di.sm_count);
-  FM_CUDA(launch_paged_attention(p, tk, tv, grid, counts, list, words, static_cast<cudaStream_t>(stream)));
+  FM_CUDA(launch_paged_attention(p, tk, tv, grid, plan, static_cast<cudaStream_t>(stream)));
   return FLASHMASK_OK;
 }
 

@@ -31,14 +31,11 @@
 //      o   = sum (p s)(c - 8) + sum p (m + 8 s)
 //    The contraction may run over the head's values in any order as long as
 //    both sides agree, so each thread takes whole 16-byte pieces of code rows.
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "launchers.h"
 #include "paged.cuh"
 #include "sm100_primitives.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace fm {
 namespace {
@@ -113,8 +110,8 @@ template <int D, int BITS, int NT>
 struct Cfg {
   static constexpr int kKT = BITS == 16 && D == 128 ? 32 : 64;  // keys of a tile
   static constexpr int kRows = 8 * NT;
-  // consumer warps: 8 warps with the loading one leave 255 registers a thread
-  static constexpr int kWarps = NT == 4 ? 4 : NT == 2 ? 7 : 8;
+  // Consumer warps.  Registers: up to 7 with the loading warp leave 255 a thread.
+  static constexpr int kWarps = BITS == 16 ? (NT == 4 ? 4 : NT == 2 ? 5 : 6) : (NT == 4 ? 4 : NT == 2 ? 7 : 8);
   static constexpr int kThreads = 32 * kWarps + 32;
   static constexpr bool kQShared = NT == 4;                     // Q fragments in shared memory
   static constexpr int kRowBytes = BITS == 16 ? 2 * D : D / 2;
@@ -124,19 +121,21 @@ struct Cfg {
   static constexpr int kStride = D + 4;                         // floats between rows of the merge buffer
   static constexpr int kMerge = kWarps * kRows * kStride * 4;
   static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
-  static constexpr int kPerStage = kStage + kKT * 4 + 16 + 16;  // + words, header, two barriers
+  static constexpr int kPerStage = kStage + 16 + 16;            // + header, two barriers
   static constexpr int kFixed = kMerge + kQBytes + 3 * kWarps * kRows * 4 + kRows * 4 + 1024 + 256;
-  static constexpr int kMaxStages = (225 * 1024 - kFixed) / kPerStage;
-  static constexpr int kStages = kMaxStages > 16 ? 16 : kMaxStages;
+  // Stages: a multiple of the warps, so that a stage's tiles all go to one warp.  (A parity wait tells a
+  // phase only from its neighbours: a warp that waited for a stage whose tile before belongs to another
+  // warp, and is still on its way, would pass a phase early.)
+  static constexpr int kFit = (225 * 1024 - kFixed) / kPerStage / kWarps;
+  static constexpr int kStages = kWarps * (kFit > 4 ? 4 : kFit);
   static constexpr int kSmem = kFixed + kStages * kPerStage;
-  static_assert(kStages >= 4, "ring too short");
+  static_assert(kFit >= 2, "ring too short");
 };
 
 template <int D, int BITS, int NT>
 struct Smem {
   using C = Cfg<D, BITS, NT>;
   uint8_t* stage;      // kStages x kStage, 1024-byte aligned for the swizzle
-  uint32_t* words;     // kStages x kKT row-visibility words
   int4* hdr;           // kStages: first key, masked, valid boxes
   uint64_t *full, *empty;
   float* merge;        // kWarps x kRows x kStride
@@ -151,7 +150,6 @@ struct Smem {
     stage = x; x += C::kStages * C::kStage;
     merge = reinterpret_cast<float*>(x); x += C::kMerge;
     q = reinterpret_cast<uint2*>(x); x += C::kQBytes;
-    words = reinterpret_cast<uint32_t*>(x); x += C::kStages * C::kKT * 4;
     hdr = reinterpret_cast<int4*>(x); x += C::kStages * 16;
     full = reinterpret_cast<uint64_t*>(x); x += C::kStages * 8;
     empty = reinterpret_cast<uint64_t*>(x); x += C::kStages * 8;
@@ -272,15 +270,13 @@ __device__ void produce(const PagedAttnParams& p, const CUtensorMap* tk, const C
         const int tv_ = __shfl_sync(0xffffffffu, valid, x);
         const int pg0 = __shfl_sync(0xffffffffu, page[0], x), pg1 = __shfl_sync(0xffffffffu, page[1], x);
         const int pg2 = __shfl_sync(0xffffffffu, page[2], x), pg3 = __shfl_sync(0xffffffffu, page[3], x);
-        const bool words = p.words_shared && tm;
         int go = 1;
         if (lane == 0) {
           if (n >= (uint32_t)C::kStages)
             go = mbar_wait(&sm.empty[stage], ((n / C::kStages) & 1u) ^ 1u, wc);
           if (go) {
             sm.hdr[stage] = make_int4(tj, tm, tv_, 0);
-            const uint32_t bytes = __popc(tv_) * (2 * box * C::kRowBytes + (BITS == 4 ? 8 * box : 0)) +
-                                   (words ? KT * 4 : 0);
+            const uint32_t bytes = __popc(tv_) * (2 * box * C::kRowBytes + (BITS == 4 ? 8 * box : 0));
             mbar_arrive_expect_tx(&sm.full[stage], bytes);
           }
         }
@@ -306,8 +302,6 @@ __device__ void produce(const PagedAttnParams& p, const CUtensorMap* tk, const C
                       (part == 3 ? p.pg.v_scales : p.pg.k_scales) + row, box * 4, &sm.full[stage]);
           }
         }
-        if (words && lane == 31)
-          bulk_load(sm.words + stage * KT, p.words + (int64_t)it.b * p.words_stride + tj, KT * 4, &sm.full[stage]);
       }
     }
   } while (ok && wk.next(p));
@@ -505,7 +499,7 @@ __device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, W
             for (int hf = 0; hf < 2; ++hf) {
               const int key = key_of(m2, hf), j = hd.x + key;
               const bool there = (hd.z >> (key >> box_shift)) & 1;
-              const uint32_t w = p.words_shared ? sm.words[stage * KT + key] : 0u;
+              const uint32_t w = p.words_shared && there ? p.words[(int64_t)it.b * p.words_stride + j] : 0u;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -955,10 +949,10 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
 }
 
 // ---------------------------------------------------------------------------
-// plan: row-visibility words and the list of visible tiles (one cluster of 8
-// CTAs per group)
+// plan: row-visibility words and tile flags (one warp per tile), then the list
+// of visible tiles (one CTA per group)
 // ---------------------------------------------------------------------------
-constexpr int kPlanCtas = 8, kPlanThreads = 256, kPlanTiles = 2048;  // tiles of one CTA at a time
+constexpr int kPlanTiles = 64;  // tiles of one CTA (8 warps)
 
 // Rows [p0, p0 + 32) with [lo, hi) cut out, as a word.
 __device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t p0) {
@@ -967,84 +961,79 @@ __device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t p0) 
 }
 
 template <int KT>
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    paged_plan_kernel(const __grid_constant__ PagedAttnParams p, int* counts, int* list, uint32_t* words) {
-  __shared__ uint8_t flag[kPlanTiles];
-  __shared__ int cnt, wsum[kPlanThreads / 32];
+__global__ void __launch_bounds__(256) paged_plan_kernel(const __grid_constant__ PagedAttnParams p, PlanOut out) {
+  griddep_wait();
   griddep_launch_dependents();
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank(), g = blockIdx.x / kPlanCtas;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = blockIdx.x / out.chunks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = group_batch(p, g);
   const int hm0 = p.per_head ? (g % p.pg.Hkv) * p.G : 0, nh = p.per_head ? p.G : 1;
   int len;
   int64_t first;
   const int hi = key_bound(p, b, &len, &first);
   const int tiles = (hi + KT - 1) / KT;
-  int done = 0;
-  for (int t0 = 0; t0 < tiles; t0 += kPlanCtas * kPlanTiles) {
-    const int block = min(tiles - t0, kPlanCtas * kPlanTiles);
-    const int share = (block + kPlanCtas - 1) / kPlanCtas;
-    const int a = min(rank * share, block), n = min(share, block - a);  // this CTA's tiles: t0 + a + [0, n)
-    int seen = 0;
-    for (int t = warp; t < n; t += kPlanThreads / 32) {
-      const int j0 = (t0 + a + t) * KT;
-      bool any = false, all = true;
+#pragma unroll 2
+  for (int x = warp; x < kPlanTiles; x += 8) {
+    const int t = (blockIdx.x % out.chunks) * kPlanTiles + x;
+    if (t >= tiles) break;
+    bool any = false, all = true;
 #pragma unroll
-      for (int jj = 0; jj < KT; jj += 32) {
-        const int j = j0 + jj + lane;
-        for (int h = 0; h < nh; ++h) {
-          const int64_t at = ((int64_t)b * p.Hm + hm0 + h);
-          int lts = 0, lte = 0, uts = 0, ute = 0;
-          if (j < p.Nm && j < hi) {
-            const int64_t m = at * p.Nm + j;
-            if (p.lts) {
-              lts = p.lts[m];
-              lte = p.lte[m];
-            }
-            if (p.uts) {
-              uts = p.uts[m];
-              ute = p.ute[m];
-            }
+    for (int jj = 0; jj < KT; jj += 32) {
+      const int j = t * KT + jj + lane;
+      for (int h = 0; h < nh; ++h) {
+        const int64_t at = ((int64_t)b * p.Hm + hm0 + h);
+        int lts = 0, lte = 0, uts = 0, ute = 0;
+        if (j < p.Nm && j < hi) {
+          const int64_t m = at * p.Nm + j;
+          if (p.lts) {
+            lts = p.lts[m];
+            lte = p.lte[m];
           }
-          for (int w = 0; w < p.n_words; ++w) {
-            const int64_t p0 = first + 32 * w;
-            const uint32_t rows = bit_range(0, min(32, p.Nq - 32 * w));
-            uint32_t see = 0;
-            if (j < hi) {
-              uint32_t hid = rows_in(lts, lte, p0) | rows_in(uts, ute, p0);
-              if (p.causal) hid |= rows_in(p0, j, p0);
-              see = rows & ~hid;
-            }
-            words[(at * p.n_words + w) * p.words_stride + j] = see;
-            any |= see != 0;
-            all &= see == rows;
+          if (p.uts) {
+            uts = p.uts[m];
+            ute = p.ute[m];
           }
         }
+        for (int w = 0; w < p.n_words; ++w) {
+          const int64_t p0 = first + 32 * w;
+          const uint32_t rows = bit_range(0, min(32, p.Nq - 32 * w));
+          uint32_t see = 0;
+          if (j < hi) {
+            uint32_t hid = rows_in(lts, lte, p0) | rows_in(uts, ute, p0);
+            if (p.causal) hid |= rows_in(p0, j, p0);
+            see = rows & ~hid;
+          }
+          out.words[(at * p.n_words + w) * p.words_stride + j] = see;
+          any |= see != 0;
+          all &= see == rows;
+        }
       }
-      any = __any_sync(0xffffffffu, any);
-      all = __all_sync(0xffffffffu, all);
-      if (lane == 0) flag[t] = any ? (all ? 2 : 1) : 0;
-      seen += any;
     }
-    if (lane == 0) wsum[warp] = seen;
-    __syncthreads();
-    if (tid == 0) {
-      int s = 0;
-      for (int i = 0; i < kPlanThreads / 32; ++i) s += wsum[i];
-      cnt = s;
+    any = __any_sync(0xffffffffu, any);
+    all = __all_sync(0xffffffffu, all);
+    if (lane == 0) out.flags[(int64_t)g * p.list_stride + t] = any ? (all ? 2 : 1) : 0;
+  }
+}
+
+__global__ void __launch_bounds__(1024) paged_list_kernel(const __grid_constant__ PagedAttnParams p, PlanOut out) {
+  __shared__ int wsum[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int len;
+  int64_t first;
+  const int hi = key_bound(p, group_batch(p, g), &len, &first);
+  const int tiles = (hi + p.tile_keys - 1) / p.tile_keys;
+  const uint8_t* flags = out.flags + (int64_t)g * p.list_stride;
+  int* list = out.list + (int64_t)g * p.list_stride;
+  int done = 0;
+  for (int t0 = 0; t0 < tiles; t0 += 4096) {  // four tiles a thread at a time
+    int f[4], mine = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int t = t0 + 4 * tid + x;
+      f[x] = t < tiles ? flags[t] : 0;
+      mine += f[x] != 0;
     }
-    cl.sync();
-    int at = done, total = 0;
-    for (int r = 0; r < kPlanCtas; ++r) {
-      const int c = *cl.map_shared_rank(&cnt, r);
-      if (r < rank) at += c;
-      total += c;
-    }
-    // this CTA's visible tiles in order
-    const int each = (n + kPlanThreads - 1) / kPlanThreads, ta = min(tid * each, n), tb = min(ta + each, n);
-    int mine = 0;
-    for (int t = ta; t < tb; ++t) mine += flag[t] != 0;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1053,14 +1042,17 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    for (int i = 0; i < warp; ++i) at += wsum[i];
-    at += incl - mine;
-    for (int t = ta; t < tb; ++t)
-      if (flag[t]) list[(int64_t)g * p.list_stride + at++] = ((t0 + a + t) << 1) | (flag[t] == 1);
-    done += total;
-    cl.sync();  // every CTA has read the counts, and this one's flags and sums are free again
+    int at = done + incl - mine;
+    for (int i = 0; i < 32; ++i) {
+      if (i < warp) at += wsum[i];
+      done += wsum[i];
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (f[x]) list[at++] = ((t0 + 4 * tid + x) << 1) | (f[x] == 1);
+    __syncthreads();
   }
-  if (rank == 0 && tid == 0) counts[g] = done;
+  if (tid == 0) out.counts[g] = done;
 }
 
 }  // namespace
@@ -1086,13 +1078,18 @@ static cudaError_t launch_variant(const PagedAttnParams& p, const CUtensorMap& t
 int paged_tile_keys(int d, int bits) { return bits == 16 && d == 128 ? 32 : 64; }
 
 cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                                   int* counts, int* list, uint32_t* words, cudaStream_t st) {
+                                   PlanOut plan, cudaStream_t st) {
   if (p.list) {
-    note_launch();
-    const unsigned blocks = (unsigned)p.n_groups * kPlanCtas;
-    if (p.tile_keys == 32) paged_plan_kernel<32><<<blocks, kPlanThreads, 0, st>>>(p, counts, list, words);
-    else paged_plan_kernel<64><<<blocks, kPlanThreads, 0, st>>>(p, counts, list, words);
-    const cudaError_t e = cudaGetLastError();
+    plan.chunks = (p.list_stride + kPlanTiles - 1) / kPlanTiles;
+    if (plan.chunks > 0) {
+      const unsigned blocks = (unsigned)plan.chunks * p.n_groups;
+      note_launch();
+      if (p.tile_keys == 32) paged_plan_kernel<32><<<blocks, 256, 0, st>>>(p, plan);
+      else paged_plan_kernel<64><<<blocks, 256, 0, st>>>(p, plan);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    const cudaError_t e = launch_after(paged_list_kernel, dim3(p.n_groups), dim3(1024), 0, st, p, plan);
     if (e != cudaSuccess) return e;
   }
 #define FM_PAGED(D, BITS)                                                              \

@@ -239,6 +239,39 @@ def test_attention_long(bits):
 
 
 @pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("cap", [1, 2, 5])
+@pytest.mark.parametrize("kind,Nq,G,d,page", [
+    ("none", 1, 4, 128, 64), ("none", 1, 4, 64, 16), ("none", 4, 4, 128, 32), ("none", 8, 4, 64, 128),
+    ("doc", 1, 4, 128, 64), ("random", 2, 4, 64, 32), ("tiles", 3, 4, 128, 16), ("random", 8, 4, 128, 64),
+])
+def test_attention_few_ctas_walk_many_items(bits, cap, kind, Nq, G, d, page):
+    """Runs that hold many items and go round the ring of tiles several times."""
+    lens = [900, 0, 33, 1300, 64, 257]
+    cache, q = Cache(23, lens, 2, d, page, bits).cuda(), case_q(6, Nq, 2 * G, d)
+    vec = (None,) * 4 if kind == "none" else masks(kind, 6, 1, 1300, 8, Nq)
+    fm.set_max_ctas(cap)
+    try:
+        check_attention(q, cache, lens, vec)
+    finally:
+        fm.set_max_ctas(0)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("kind", ["none", "doc"])
+def test_attention_calls_in_a_row(bits, kind):
+    """Calls queued without waiting between them give the bits of single calls."""
+    lens = [1500, 300, 4000]
+    cache, q = Cache(24, lens, 2, 128, 64, bits).cuda(), case_q(3, 1, 8, 128)
+    vec = (None,) * 4 if kind == "none" else masks(kind, 3, 1, 4000, 8, 1)
+    n = i32(lens)
+    o, lse = fm.paged_attention(q, cache.k, cache.v, cache.table, n, *vec, **cache.kw)
+    torch.cuda.synchronize()
+    outs = [fm.paged_attention(q, cache.k, cache.v, cache.table, n, *vec, **cache.kw) for _ in range(40)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, o) and torch.equal(b, lse) for a, b in outs)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
 def test_attention_bad_entries_are_reported_and_left_out(bits):
     lens = [100, 70]
     cache, q = Cache(20, lens, 2, 64, 16, bits).cuda(), case_q(2, 1, 2, 64)
