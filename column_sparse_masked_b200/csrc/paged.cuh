@@ -52,6 +52,7 @@ struct PagedAttnParams {
   // work: groups (a sequence, or a sequence and KV head with per-head masks) of `mult` items of `rows` rows
   int per_head, n_groups, mult, n_rb, rows, tile_keys;
   int min_tiles;            // units that a run holds at least
+  int uncut;                // one CTA per item, no parts
   // plan (with mask vectors): visible tiles of each group, row-visibility words of each key
   const int* counts;        // [n_groups]
   const int* list;          // [n_groups, list_stride]: tile << 1 | some pair hidden

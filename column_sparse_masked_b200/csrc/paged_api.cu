@@ -72,6 +72,8 @@ int check_paged_rows(const flashmask_pages* pg, const flashmask_paged_rows* r) {
   }
   // work items are numbered in 32 bits
   if ((int64_t)pg->B * r->Nq * r->Hq > INT_MAX / 4) return FLASHMASK_ERR_UNSUPPORTED;
+  const int64_t tiles = ((int64_t)pg->table_width * pg->page_size + 31) / 32, blocks = ((int64_t)r->Nq * (r->Hq / pg->Hkv) + 7) / 8;
+  if (blocks * pg->Hkv * pg->B > INT_MAX / 2 / (tiles > 0 ? tiles : 1)) return FLASHMASK_ERR_UNSUPPORTED;
   return FLASHMASK_OK;
 }
 
@@ -110,15 +112,16 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
   return L;
 }
 
-// 2-D map over the rows of all pages: box = 64 values x box_rows rows, 128-byte swizzle.
+// Map over the rows of all pages as {64 values, row, 64-value part}: a box holds box_rows whole
+// rows, part by part, with 128-byte swizzle.
 int make_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int d, int box_rows) {
   auto enc = encode_fn();
   if (!enc) return FLASHMASK_ERR_CUDA;
-  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  cuuint32_t es[2] = {1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, es,
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(d / 64)};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)(d / 64)};
+  cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FLASHMASK_OK : cuda_status(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
@@ -226,6 +229,10 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
   p.rows = L.rows;
   p.tile_keys = L.tile_keys;
   p.min_tiles = 8;
+  // One CTA per item, and no second kernel, where splitting has nothing to give: all items fit the device
+  // at once and the table itself bounds them to a few tiles per warp.
+  const int64_t items = (int64_t)L.n_groups * L.mult;
+  p.uncut = items <= di.sm_count && L.keys / L.tile_keys <= 16;
   p.part = reinterpret_cast<float*>(ws + L.part);
   p.stat = reinterpret_cast<float2*>(ws + L.stat);
   p.meta = reinterpret_cast<int*>(ws + L.meta);
@@ -248,7 +255,7 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
     FM_TRY(make_rows_map(&tk, pages->k, rows, pages->d, box));
     FM_TRY(make_rows_map(&tv, pages->v, rows, pages->d, box));
   }
-  const int grid = persistent_grid(kPagedMaxCtas, di.sm_count);
+  const int grid = p.uncut ? (int)items : persistent_grid(kPagedMaxCtas, di.sm_count);
   FM_CUDA(launch_paged_attention(p, tk, tv, grid, plan, static_cast<cudaStream_t>(stream)));
   return FLASHMASK_OK;
 }

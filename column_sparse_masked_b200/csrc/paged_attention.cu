@@ -68,13 +68,9 @@ __device__ __forceinline__ int tiles_of(const PagedAttnParams& p, int g) {
 // A run of units, walked segment by segment (a segment: tiles [t, t + n) of
 // one item).  Every warp of the CTA walks it the same way.
 struct Walk {
-  int g, in, t, T;   // group, item in the group, first tile, tiles of the group's items
-  int64_t left;      // units left in the run
-  int n;             // tiles of this segment
-  __device__ __forceinline__ void begin(const PagedAttnParams& p) {
-    T = tiles_of(p, g);
-    n = (int)min((int64_t)(T - t), left);
-  }
+  int g, in, t, T;  // group, item in the group, first tile, tiles of the group's items
+  int left;         // units left in the run
+  int n;            // tiles of this segment
   __device__ __forceinline__ bool next(const PagedAttnParams& p) {
     left -= n;
     if (left <= 0) return false;
@@ -86,7 +82,7 @@ struct Walk {
         T = tiles_of(p, g);
       } while (T == 0);
     }
-    n = (int)min((int64_t)T, left);
+    n = min(T, left);
     return true;
   }
 };
@@ -110,9 +106,8 @@ template <int D, int BITS, int NT>
 struct Cfg {
   static constexpr int kKT = BITS == 16 && D == 128 ? 32 : 64;  // keys of a tile
   static constexpr int kRows = 8 * NT;
-  // Consumer warps.  Registers: up to 7 with the loading warp leave 255 a thread.
   static constexpr int kWarps = BITS == 16 ? (NT == 4 ? 4 : NT == 2 ? 5 : 6) : (NT == 4 ? 4 : NT == 2 ? 7 : 8);
-  static constexpr int kThreads = 32 * kWarps + 32;
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr bool kQShared = NT == 4;                     // Q fragments in shared memory
   static constexpr int kRowBytes = BITS == 16 ? 2 * D : D / 2;
   static constexpr int kHalf = kKT * kRowBytes;                 // K or V part of a stage
@@ -121,28 +116,28 @@ struct Cfg {
   static constexpr int kStride = D + 4;                         // floats between rows of the merge buffer
   static constexpr int kMerge = kWarps * kRows * kStride * 4;
   static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
-  static constexpr int kPerStage = kStage + 16 + 16;            // + header, two barriers
+  static constexpr int kPerStage = kStage + 16 + 8;             // + header, barrier
   static constexpr int kFixed = kMerge + kQBytes + 3 * kWarps * kRows * 4 + kRows * 4 + 1024 + 256;
-  // Stages: a multiple of the warps, so that a stage's tiles all go to one warp.  (A parity wait tells a
-  // phase only from its neighbours: a warp that waited for a stage whose tile before belongs to another
-  // warp, and is still on its way, would pass a phase early.)
+  // Every warp has a ring of its own, which it fills and empties itself: a stage is refilled by the warp
+  // that has just read it, so nothing waits for another warp between the ends of items.
   static constexpr int kFit = (225 * 1024 - kFixed) / kPerStage / kWarps;
-  static constexpr int kStages = kWarps * (kFit > 4 ? 4 : kFit);
+  static constexpr int kDepth = kFit > 4 ? 4 : kFit;
+  static constexpr int kStages = kWarps * kDepth;
   static constexpr int kSmem = kFixed + kStages * kPerStage;
-  static_assert(kFit >= 2, "ring too short");
+  static constexpr int kBoxes = kKT / 16;                       // copies of a tile's rows at most
+  static_assert(kDepth >= 2, "ring too short");
 };
 
 template <int D, int BITS, int NT>
 struct Smem {
   using C = Cfg<D, BITS, NT>;
   uint8_t* stage;      // kStages x kStage, 1024-byte aligned for the swizzle
-  int4* hdr;           // kStages: first key, masked, valid boxes
-  uint64_t *full, *empty;
+  int4* hdr;           // kStages: first key, some pair hidden, valid boxes
+  uint64_t* full;      // kStages
   float* merge;        // kWarps x kRows x kStride
   uint2* q;            // Q fragments (kQShared)
   float *m, *l, *c;    // kWarps x kRows
   float* qsum;         // kRows
-  long long* scan;     // prologue
   int* abort;
   __device__ __forceinline__ explicit Smem(uint8_t* raw) {
     const uint32_t a = smem_addr(raw);
@@ -152,8 +147,6 @@ struct Smem {
     q = reinterpret_cast<uint2*>(x); x += C::kQBytes;
     hdr = reinterpret_cast<int4*>(x); x += C::kStages * 16;
     full = reinterpret_cast<uint64_t*>(x); x += C::kStages * 8;
-    empty = reinterpret_cast<uint64_t*>(x); x += C::kStages * 8;
-    scan = reinterpret_cast<long long*>(x); x += 16 * 8;
     m = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
     l = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
     c = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
@@ -184,11 +177,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+// Box of rows of one head in one page: [D/64][rows][64 values] in shared memory.
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int row) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %3}], [%2];" ::"r"(
           smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(row)
       : "memory");
 }
 
@@ -219,109 +213,134 @@ __device__ __forceinline__ float sum8(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
+// Fills one warp's ring: the tiles of the CTA's run that are the warp's, in
+// order, across segments.  Pages are looked up for 32 of them at a time, one
+// by each lane.
 template <int D, int BITS, int NT>
-__device__ void produce(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
-                        const Smem<D, BITS, NT>& sm, Walk wk, const WaitCtx& wc) {
+struct Issuer {
   using C = Cfg<D, BITS, NT>;
-  constexpr int KT = C::kKT;
-  const int lane = threadIdx.x & 31;
-  const int box = min(KT, 1 << p.pg.page_shift);  // rows of one copy: part of one page
-  const int boxes = KT / box, box_shift = __ffs(box) - 1;
-  uint32_t n = 0;
-  bool ok = true;
-  do {
-    const Item it = item_of(p, wk.g, wk.in, C::kRows);
+  Walk w;
+  int k;        // the warp's next tile that is not in the batch, in the segment
+  int x, nb;    // next tile of the batch, and its size
+  int issued;
+  bool more;
+  int kvh;
+  int j0, flags, page[C::kBoxes];  // a lane's tile: first key, masked | valid boxes << 1, pages
+
+  __device__ __forceinline__ void batch(const PagedAttnParams& p) {
+    constexpr int KT = C::kKT;
+    const int lane = threadIdx.x & 31, box_shift = min(p.pg.page_shift, KT == 32 ? 5 : 6);
+    const int boxes = KT >> box_shift;
+    const Item it = item_of(p, w.g, w.in, C::kRows);
+    kvh = it.kvh;
     int len;
     int64_t first;
     const int hi = key_bound(p, it.b, &len, &first);
-    // keys that every row of the item sees, without mask vectors
-    const int64_t row_first = first + it.row0 / p.G;
-    const int64_t all = p.causal ? min((int64_t)len, row_first + 1) : (int64_t)len;
-    for (int k0 = 0; k0 < wk.n && ok; k0 += 32) {
-      // 32 tiles at a time: each lane looks up one tile and its pages
-      int j0 = 0, masked = 0, valid = 0, page[4];
-      const int k = k0 + lane;
+    nb = min(32, (w.n - k + C::kWarps - 1) / C::kWarps);
+    x = 0;
+    j0 = 0;
+    int masked = 0, valid = 0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) page[x] = 0;
-      if (k < wk.n) {
-        const int t = wk.t + k;
-        if (p.list) {
-          const int e = p.list[(int64_t)wk.g * p.list_stride + t];
-          j0 = (e >> 1) * KT;
-          masked = e & 1;
-        } else {
-          j0 = t * KT;
-          masked = (int64_t)j0 + KT > all;
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int j = j0 + (x << box_shift);
-          if (x < boxes && j < hi) {
-            page[x] = page_of(p.pg, it.b, j);
-            if (page[x] >= 0) valid |= 1 << x;
-          }
-        }
-        if (valid != (1 << boxes) - 1) masked = 1;
+    for (int i = 0; i < C::kBoxes; ++i) page[i] = 0;
+    if (lane < nb) {
+      const int t = w.t + k + lane * C::kWarps;
+      if (p.list) {
+        const int e = p.list[(int64_t)w.g * p.list_stride + t];
+        j0 = (e >> 1) * KT;
+        masked = e & 1;
+      } else {
+        j0 = t * KT;
+        // keys that every row of the item sees
+        const int64_t all = p.causal ? min((int64_t)len, first + it.row0 / p.G + 1) : (int64_t)len;
+        masked = (int64_t)j0 + KT > all;
       }
-      const int m = min(32, wk.n - k0);
-      for (int x = 0; x < m; ++x, ++n) {
-        const int stage = n % C::kStages;
-        const int tj = __shfl_sync(0xffffffffu, j0, x), tm = __shfl_sync(0xffffffffu, masked, x);
-        const int tv_ = __shfl_sync(0xffffffffu, valid, x);
-        const int pg0 = __shfl_sync(0xffffffffu, page[0], x), pg1 = __shfl_sync(0xffffffffu, page[1], x);
-        const int pg2 = __shfl_sync(0xffffffffu, page[2], x), pg3 = __shfl_sync(0xffffffffu, page[3], x);
-        int go = 1;
-        if (lane == 0) {
-          if (n >= (uint32_t)C::kStages)
-            go = mbar_wait(&sm.empty[stage], ((n / C::kStages) & 1u) ^ 1u, wc);
-          if (go) {
-            sm.hdr[stage] = make_int4(tj, tm, tv_, 0);
-            const uint32_t bytes = __popc(tv_) * (2 * box * C::kRowBytes + (BITS == 4 ? 8 * box : 0));
-            mbar_arrive_expect_tx(&sm.full[stage], bytes);
-          }
+#pragma unroll
+      for (int i = 0; i < C::kBoxes; ++i) {
+        const int j = j0 + (i << box_shift);
+        if (i < boxes && j < hi) {
+          page[i] = page_of(p.pg, it.b, j);
+          if (page[i] >= 0) valid |= 1 << i;
         }
-        ok = __shfl_sync(0xffffffffu, go, 0);
-        if (!ok) break;
-        // copy c: box c / 4, part c % 4
-        const int bx = lane >> 2, part = lane & 3;
-        uint8_t* st = sm.stage + stage * C::kStage;
-        if (bx < boxes && ((tv_ >> bx) & 1)) {
-          const int pid = bx == 0 ? pg0 : bx == 1 ? pg1 : bx == 2 ? pg2 : pg3;
-          const int64_t row = row_of(p.pg, pid, it.kvh, tj + (bx << box_shift));
-          if (BITS == 16) {
-            if (part < D / 32) {
-              const int half = part & (D / 64 - 1), is_v = part / (D / 64);
-              tma_load_2d(st + is_v * C::kHalf + half * (KT * 128) + (bx << box_shift) * 128, is_v ? tv : tk,
-                          &sm.full[stage], half * 64, (int)row);
-            }
-          } else if (part < 2) {
-            bulk_load(st + part * C::kHalf + (bx << box_shift) * C::kRowBytes,
-                      (part ? p.pg.v : p.pg.k) + row * C::kRowBytes, box * C::kRowBytes, &sm.full[stage]);
-          } else {
-            bulk_load(st + 2 * C::kHalf + (part - 2) * C::kScales + (bx << box_shift) * 4,
-                      (part == 3 ? p.pg.v_scales : p.pg.k_scales) + row, box * 4, &sm.full[stage]);
-          }
+      }
+      if (valid != (1 << boxes) - 1) masked = 1;
+    }
+    flags = masked | (valid << 1);
+    k += nb * C::kWarps;
+  }
+
+  __device__ __forceinline__ void start(const PagedAttnParams& p, const Walk& wk, int warp) {
+    w = wk;
+    k = warp;
+    issued = 0;
+    x = nb = 0;
+    more = true;
+  }
+
+  __device__ __forceinline__ void issue(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
+                                        const Smem<D, BITS, NT>& sm, int warp) {
+    if (x == nb) {
+      if (!more) return;
+      while (k >= w.n) {
+        k -= w.n;
+        if (!w.next(p)) {
+          more = false;
+          x = nb = 0;
+          return;
         }
+      }
+      batch(p);
+    }
+    constexpr int KT = C::kKT;
+    const int lane = threadIdx.x & 31, box_shift = min(p.pg.page_shift, KT == 32 ? 5 : 6);
+    const int tj = __shfl_sync(0xffffffffu, j0, x), f = __shfl_sync(0xffffffffu, flags, x);
+    const int bx = BITS == 16 ? lane >> 1 : lane >> 2;  // a copy per lane
+    int pid = 0;
+#pragma unroll
+    for (int i = 0; i < C::kBoxes; ++i) {
+      const int v = __shfl_sync(0xffffffffu, page[i], x);
+      if (i == bx) pid = v;
+    }
+    ++x;
+    const int stage = warp * C::kDepth + issued % C::kDepth;
+    ++issued;
+    uint64_t* bar = &sm.full[stage];
+    if (lane == 0) {
+      sm.hdr[stage] = make_int4(tj, f & 1, f >> 1, 0);
+      mbar_arrive_expect_tx(bar, (uint32_t)(__popc(f >> 1) << box_shift) * (2 * C::kRowBytes + (BITS == 4 ? 8 : 0)));
+    }
+    __syncwarp();
+    if (bx < C::kBoxes && ((f >> (1 + bx)) & 1)) {
+      const int64_t row = row_of(p.pg, pid, kvh, tj + (bx << box_shift));
+      uint8_t* st = sm.stage + stage * C::kStage;
+      if (BITS == 16) {
+        tma_load_rows(st + (lane & 1) * C::kHalf + (bx << box_shift) * C::kRowBytes, (lane & 1) ? tv : tk, bar,
+                      (int)row);
+      } else {
+        const int part = lane & 3;  // K codes, V codes, K scales, V scales
+        const uint8_t* src = part == 0 ? p.pg.k : part == 1 ? p.pg.v
+                             : reinterpret_cast<const uint8_t*>(part == 2 ? p.pg.k_scales : p.pg.v_scales);
+        const int rb = part < 2 ? C::kRowBytes : 4;
+        const int at = (part & 1) * (part < 2 ? C::kHalf : C::kScales) + (part < 2 ? 0 : 2 * C::kHalf);
+        bulk_load(st + at + (bx << box_shift) * rb, src + row * rb, (uint32_t)rb << box_shift, bar);
       }
     }
-  } while (ok && wk.next(p));
-  if (!ok && lane == 0) {  // gave up: let the copies in flight land before the CTA ends
-    WaitCtx w2 = wc;
-    int zero = 0;
-    w2.abort = &zero;
-    const uint32_t from = n > (uint32_t)C::kStages ? n - C::kStages : 0u;
-    for (uint32_t i = from; i < n; ++i) mbar_wait(&sm.full[i % C::kStages], (i / C::kStages) & 1u, w2);
   }
-}
+};
 
 template <int D, int BITS, int NT>
-__device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, Walk wk, const WaitCtx& wc) {
+__device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
+                                       const Smem<D, BITS, NT>& sm, Walk wk, const WaitCtx& wc) {
   using C = Cfg<D, BITS, NT>;
   constexpr int KT = C::kKT, MT = D / 16, KS = D / 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, q4 = lane & 3;  // the fragment's row in a block of 8, and its column pair
   const int box_shift = min(p.pg.page_shift, KT == 32 ? 5 : 6);
-  uint32_t base = 0;
+  const uint32_t box_rows = 1u << box_shift;
+  Issuer<D, BITS, NT> is;
+  is.start(p, wk, warp);
+#pragma unroll 1
+  for (int i = 0; i < C::kDepth; ++i) is.issue(p, tk, tv, sm, warp);
+  int k = warp, taken = 0;  // the warp's next tile in the segment, and the tiles it has taken
   bool alive = true, first_seg = true;
   do {
     const Item it = item_of(p, wk.g, wk.in, C::kRows);
@@ -381,7 +400,7 @@ __device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, W
         }
         if (lane < C::kRows) sm.qsum[lane] = s;
       }
-      named_barrier_sync(1, 32 * C::kWarps);
+      __syncthreads();
       if (BITS == 4) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -405,16 +424,23 @@ __device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, W
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
 
-    const uint32_t end = base + wk.n;
-    for (uint32_t n = base + ((uint32_t)warp + C::kWarps - base % C::kWarps) % C::kWarps; n < end; n += C::kWarps) {
-      const int stage = n % C::kStages;
-      if (alive) alive = mbar_wait(&sm.full[stage], (n / C::kStages) & 1u, wc);
+    for (; k < wk.n; k += C::kWarps) {
+      const int stage = warp * C::kDepth + taken % C::kDepth;
+      if (alive) alive = mbar_wait(&sm.full[stage], (taken / C::kDepth) & 1u, wc);
       alive = __all_sync(0xffffffffu, alive);
       if (!alive) continue;  // keeps walking: the barriers at the ends of segments are still met
+      ++taken;
       const int4 hd = sm.hdr[stage];
       uint8_t* st = sm.stage + stage * C::kStage;
       const uint32_t kaddr = smem_addr(st), vaddr = kaddr + C::kHalf;
       bool wrote = false;
+      // bf16 rows lie [box][64-value part][row of the box]: bytes to the 16 rows from `key` on
+      auto block16 = [&](int key) {
+        return (uint32_t)((key >> box_shift) << box_shift) * C::kRowBytes + (key & (box_rows - 1)) * 128u;
+      };
+      auto chunk_at = [&](int key, int ch) {  // 16-byte chunk ch of a row
+        return block16(key & ~15) + (ch >> 3) * (box_rows * 128) + (key & 15) * 128 + (((ch & 7) ^ (key & 7)) << 4);
+      };
 #pragma unroll 1
       for (int sb = 0; sb < KT; sb += 32) {
         // ---- S^T: 32 keys x rows ----
@@ -426,14 +452,14 @@ __device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, W
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[m2][nt][e] = 0.f;
         if (BITS == 16) {
-          const int key = sb + (lane & 7) + ((lane >> 3) & 1) * 8, hi = lane >> 4;
+          const uint32_t lrow = ((lane & 7) + ((lane >> 3) & 1) * 8) * 128, hi = lane >> 4;
 #pragma unroll
           for (int m2 = 0; m2 < 2; ++m2)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-              const int kk = key + m2 * 16, ch = ks * 2 + hi;
+              const uint32_t ch = ks * 2 + hi;
               uint32_t a[4];
-              ldsm4(a, kaddr + (ch >> 3) * (KT * 128) + kk * 128 + (((ch & 7) ^ (kk & 7)) << 4));
+              ldsm4(a, kaddr + block16(sb + m2 * 16) + (ks >> 2) * (box_rows * 128) + lrow + (((ch & 7) ^ (lane & 7)) << 4));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 const uint2 b = C::kQShared ? sm.q[(ks * NT + nt) * 32 + lane] : qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
@@ -588,7 +614,7 @@ __device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, W
           const __nv_bfloat162 zero = z;
 #pragma unroll
           for (int ch = 0; ch < D / 8; ++ch) {
-            const uint4 u = *reinterpret_cast<const uint4*>(st + C::kHalf + (ch >> 3) * (KT * 128) + kk * 128 + (((ch & 7) ^ (kk & 7)) << 4));
+            const uint4 u = *reinterpret_cast<const uint4*>(st + C::kHalf + chunk_at(kk, ch));
             const uint32_t ww[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&ww[y]), zero, z);
@@ -611,31 +637,30 @@ __device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, W
                   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                      const int x = mt * 16 + u * 8 + g8, ch = x >> 3, k6 = sb + k5;
+                      const int x = mt * 16 + u * 8 + g8;
                       const __nv_bfloat16 v = *reinterpret_cast<const __nv_bfloat16*>(
-                          st + C::kHalf + (ch >> 3) * (KT * 128) + k6 * 128 + (((ch & 7) ^ (k6 & 7)) << 4) + (x & 7) * 2);
+                          st + C::kHalf + chunk_at(sb + k5, x >> 3) + (x & 7) * 2);
                       acc[mt][nt][2 * u + e] = fmaf(pr, __bfloat162float(v), acc[mt][nt][2 * u + e]);
                     }
                 }
               }
             __syncwarp();
             if (lane < D / 8)
-              *reinterpret_cast<uint4*>(st + C::kHalf + (lane >> 3) * (KT * 128) + (sb + k5) * 128 + ((lane & 7) << 4)) =
-                  make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(st + C::kHalf + chunk_at(sb + k5, lane)) = make_uint4(0u, 0u, 0u, 0u);
             wrote = true;
           }
           __syncwarp();
         }
         // ---- O^T += V^T P^T ----
         if (BITS == 16) {
-          const int key = sb + (lane & 7) + (lane >> 4) * 8, hi = (lane >> 3) & 1;
+          const uint32_t lrow = ((lane & 7) + (lane >> 4) * 8) * 128, hi = (lane >> 3) & 1;
 #pragma unroll
           for (int m2 = 0; m2 < 2; ++m2)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              const int kk = key + m2 * 16, ch = mt * 2 + hi;
+              const uint32_t ch = mt * 2 + hi;
               uint32_t a[4];
-              ldsm4_t(a, vaddr + (ch >> 3) * (KT * 128) + kk * 128 + (((ch & 7) ^ (kk & 7)) << 4));
+              ldsm4_t(a, vaddr + block16(sb + m2 * 16) + (mt >> 2) * (box_rows * 128) + lrow + (((ch & 7) ^ (lane & 7)) << 4));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816(acc[mt][nt], a, pb[m2][nt][0], pb[m2][nt][1]);
             }
@@ -676,9 +701,9 @@ __device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, W
       }
       if (wrote) fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.empty[stage]);
+      is.issue(p, tk, tv, sm, warp);
     }
-    base = end;
+    k -= wk.n;
 
     // ---- the warps' sums together ----
 #pragma unroll
@@ -695,7 +720,7 @@ __device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, W
         if (BITS == 4) sm.c[r] = cor[x];
       }
     }
-    named_barrier_sync(1, 32 * C::kWarps);
+    __syncthreads();
 #pragma unroll
     for (int x = 0; x < 2 * NT; ++x) {
       const int r = (x >> 1) * 8 + 2 * q4 + (x & 1);
@@ -715,9 +740,9 @@ __device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, W
         }
       }
     }
-    named_barrier_sync(1, 32 * C::kWarps);
+    __syncthreads();
     const bool whole = wk.n == wk.T;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1);
+    const int slot = 2 * blockIdx.x + (first_seg ? 0 : 1);
     for (int x = threadIdx.x; x < C::kRows * (D / 4); x += 32 * C::kWarps) {
       const int r = x / (D / 4), d4 = x % (D / 4);
       if (r >= R) continue;
@@ -757,9 +782,31 @@ __device__ void consume(const PagedAttnParams& p, const Smem<D, BITS, NT>& sm, W
         if (d4 == 0) p.stat[slot * C::kRows + r] = make_float2(top, L);
       }
     }
-    named_barrier_sync(1, 32 * C::kWarps);
+    __syncthreads();
     first_seg = false;
   } while (wk.next(p));
+  if (!alive && lane == 0) {  // gave up: let the copies in flight land before the CTA ends
+    WaitCtx w2 = wc;
+    int zero = 0;
+    w2.abort = &zero;
+    for (int i = taken; i < is.issued; ++i)
+      mbar_wait(&sm.full[warp * C::kDepth + i % C::kDepth], (i / C::kDepth) & 1u, w2);
+  }
+}
+
+// Rows of a group (items in0 <= item < in1 of it) whose keys are all hidden or missing.
+template <int D>
+__device__ void write_empty(const PagedAttnParams& p, int g, int in0, int in1, int threads) {
+  const int b = group_batch(p, g), R = p.Nq * p.G;
+  for (int in = in0; in < in1; ++in) {
+    const Item it = item_of(p, g, in, p.rows);
+    const int n = min(p.rows, R - it.row0);
+    for (int x = threadIdx.x; x < n * (D / 8); x += threads) {
+      const int row = it.row0 + x / (D / 8), c = x % (D / 8), i = row / p.G, h = it.kvh * p.G + row % p.G;
+      *reinterpret_cast<uint4*>(p.o + (((int64_t)b * p.Nq + i) * p.Hq + h) * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+      if (c == 0) p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] = -INFINITY;
+    }
+  }
 }
 
 template <int D, int BITS, int NT>
@@ -770,114 +817,97 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
   extern __shared__ uint8_t raw[];
   Smem<D, BITS, NT> sm(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    *sm.abort = 0;
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
-    }
+  if (lane == 0) {
+    for (int i = 0; i < C::kDepth; ++i) mbar_init(&sm.full[warp * C::kDepth + i], 1);
+    if (warp == 0) *sm.abort = 0;
     fence_mbar_init();
   }
-  griddep_wait();
-  griddep_launch_dependents();
-
-  // ---- this CTA's run of units: total, then the group it begins in ----
-  const int per = (p.n_groups + C::kThreads - 1) / C::kThreads;
-  const int ga = min(tid * per, p.n_groups), gb = min(ga + per, p.n_groups);
-  long long mine = 0;
-  for (int g = ga; g < gb; ++g) mine += tiles_of(p, g);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) sm.scan[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w <= C::kWarps; ++w) {
-    if (w < warp) before += sm.scan[w];
-    total += sm.scan[w];
-  }
-  before += incl - mine;
-  total *= p.mult;
-  before *= p.mult;
-  const long long want = (total + p.min_tiles - 1) / p.min_tiles;
-  const long long ctas = want < gridDim.x ? (want > 0 ? want : 1) : gridDim.x;
-  const bool works = blockIdx.x < ctas && total > 0;
-  const long long u0 = works ? blockIdx.x * total / ctas : 0, u1 = works ? (blockIdx.x + 1) * total / ctas : 0;
-  if (u1 > u0 && mine > 0 && u0 >= before && u0 < before + mine * p.mult) {
-    long long at = before;
-    int g = ga, T = tiles_of(p, g);
-    while (u0 >= at + (long long)T * p.mult) {
-      at += (long long)T * p.mult;
-      T = tiles_of(p, ++g);
-    }
-    sm.scan[12] = g;
-    sm.scan[13] = u0 - at;
-  }
-  __syncthreads();
-
-  // rows of sequences with no visible tile
-  for (int g = blockIdx.x; g < p.n_groups; g += gridDim.x) {
-    if (tiles_of(p, g) != 0) continue;
-    const int b = group_batch(p, g), heads = p.per_head ? p.G : p.Hq, h0 = p.per_head ? (g % p.pg.Hkv) * p.G : 0;
-    for (int64_t x = tid; x < (int64_t)p.Nq * heads * (D / 8); x += C::kThreads) {
-      const int c = (int)(x % (D / 8)), h = h0 + (int)(x / (D / 8) % heads), i = (int)(x / (D / 8) / heads);
-      *reinterpret_cast<uint4*>(p.o + (((int64_t)b * p.Nq + i) * p.Hq + h) * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
-      if (c == 0) p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] = -INFINITY;
-    }
-  }
-  if (u1 <= u0) {
-    if (tid == 0) p.meta[blockIdx.x * kMetaInts] = -1;
-    return;
-  }
-
-  Walk wk;
-  wk.g = (int)sm.scan[12];
-  const long long off = sm.scan[13];
-  wk.T = tiles_of(p, wk.g);
-  wk.in = (int)(off / wk.T);
-  wk.t = (int)(off % wk.T);
-  wk.left = u1 - u0;
-  wk.n = (int)min((long long)(wk.T - wk.t), (long long)wk.left);
-
   WaitCtx wc;
   wc.abort = sm.abort;
   wc.status = p.pg.status;
   wc.limit_ns = p.wait_limit_ns;
   wc.smem_base = smem_addr(raw);
   wc.kernel = 5;
-  if (warp == C::kWarps) {
-    // an item that begins in this run and goes on in the next ones: where its parts are
-    if (lane == 0) {
-      int* meta = p.meta + blockIdx.x * kMetaInts;
-      Walk w = wk;
-      bool first = true;
-      long long u = u0;
-      while (u + w.n < u1) {
-        u += w.n;
-        first = false;
-        w.next(p);
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (p.uncut) {  // one item per CTA
+    Walk wk;
+    wk.g = blockIdx.x / p.mult;
+    wk.in = blockIdx.x % p.mult;
+    wk.t = 0;
+    wk.T = wk.n = wk.left = tiles_of(p, wk.g);
+    if (wk.T == 0) write_empty<D>(p, wk.g, wk.in, wk.in + 1, C::kThreads);
+    else attend<D, BITS, NT>(p, &tk, &tv, sm, wk, wc);
+    return;
+  }
+
+  // ---- this CTA's run of units: every warp sums the groups' tiles and finds the group it begins in ----
+  const int per = (p.n_groups + 31) / 32, ga = min(lane * per, p.n_groups), gb = min(ga + per, p.n_groups);
+  int mine = 0;
+#pragma unroll 4
+  for (int g = ga; g < gb; ++g) mine += tiles_of(p, g);
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31) * p.mult;
+  // units of a run: total / ctas, one more for the first total % ctas
+  const int ctas = min((int)gridDim.x, max(1, total / p.min_tiles)), q = total / ctas, rem = total - q * ctas;
+  const int c = blockIdx.x;
+  const int u0 = c * q + min(c, rem), n_units = c < ctas ? q + (c < rem ? 1 : 0) : 0;
+  if (n_units > 0) {
+    const unsigned has = __ballot_sync(0xffffffffu, u0 < incl * p.mult);
+    const int src = __ffs(has) - 1;
+    Walk wk;
+    int at = (incl - mine) * p.mult;
+    wk.g = ga;
+    wk.T = 0;
+    if (lane == src) {
+      wk.T = tiles_of(p, wk.g);
+      while (u0 >= at + wk.T * p.mult) {
+        at += wk.T * p.mult;
+        wk.T = tiles_of(p, ++wk.g);
       }
-      if (w.t == 0 && w.n < w.T) {
-        const Item it = item_of(p, w.g, w.in, C::kRows);
-        const long long last = u + w.T - 1;
+    }
+    wk.g = __shfl_sync(0xffffffffu, wk.g, src);
+    wk.T = __shfl_sync(0xffffffffu, wk.T, src);
+    const int off = u0 - __shfl_sync(0xffffffffu, at, src);
+    wk.in = off / wk.T;
+    wk.t = off - wk.in * wk.T;
+    wk.left = n_units;
+    wk.n = min(wk.T - wk.t, n_units);
+    attend<D, BITS, NT>(p, &tk, &tv, sm, wk, wc);
+
+    // an item that begins in this run and goes on in the next ones: where its parts are
+    if (tid == 0) {
+      int* meta = p.meta + c * kMetaInts;
+      bool first = true;
+      int u = u0;
+      while (u + wk.n < u0 + n_units) {
+        u += wk.n;
+        first = false;
+        wk.next(p);
+      }
+      meta[0] = -1;
+      if (wk.t == 0 && wk.n < wk.T) {
+        const Item it = item_of(p, wk.g, wk.in, C::kRows);
+        const int last = u + wk.T - 1, big = rem * (q + 1);  // the CTA that ends it holds unit `last`
         meta[0] = it.b;
         meta[1] = it.kvh;
         meta[2] = it.row0;
-        meta[3] = (int)(((last + 1) * ctas + total - 1) / total - 1);  // the CTA that ends it
+        meta[3] = last < big ? last / (q + 1) : rem + (last - big) / q;
         meta[4] = first ? 0 : 1;
-      } else {
-        meta[0] = -1;
       }
     }
-    __syncwarp();
-    produce<D, BITS, NT>(p, &tk, &tv, sm, wk, wc);
-  } else {
-    consume<D, BITS, NT>(p, sm, wk, wc);
+  } else if (tid == 0) {
+    p.meta[c * kMetaInts] = -1;
   }
+  for (int g = c; g < p.n_groups; g += gridDim.x)
+    if (tiles_of(p, g) == 0) write_empty<D>(p, g, 0, p.mult, C::kThreads);
 }
 
 // ---------------------------------------------------------------------------
@@ -1071,7 +1101,7 @@ static cudaError_t launch_variant(const PagedAttnParams& p, const CUtensorMap& t
     k<<<grid, C::kThreads, C::kSmem, st>>>(tk, tv, p);
     e = cudaGetLastError();
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.uncut) return e;
   return launch_after(paged_merge_kernel<D, C::kRows>, dim3(grid, C::kRows), dim3(256), 0, st, p);
 }
 

@@ -1,10 +1,11 @@
-"""The paged attention kernel's ring of tiles, checked on a randomised model (CPU only).
+"""The paged attention kernel's rings of tiles, checked on a randomised model (CPU only).
 
-The producer fills stages in order, tile n goes to consumer warp n % W, copies land in any order, and the
-warps meet at the end of each segment.  The ring's length is a multiple of W, so a stage's tiles all go to
-one warp: otherwise a warp could wait for a stage whose previous tile, another warp's, has not landed yet,
-and its parity wait would pass a phase early.  The model (scheduler and barriers of protocol_model.py, which
-reject any wait whose parity is ambiguous) shows the kernel's rings to be safe and each planted mistake to be caught.
+Tile n of a CTA's run goes to warp n % W.  Every warp has a ring of its own: it fills the stages with its first
+tiles, and refills a stage with its next tile when it has read it; copies land in any order, and the warps
+meet at the end of each segment while their rings run on into the next.  The model (scheduler and barriers of
+protocol_model.py, which reject any wait whose parity is ambiguous) shows this to be safe and planted mistakes
+to be caught, among them one ring shared by all warps: there a stage's tiles belong to different warps, and a warp
+could wait for a stage whose previous tile has not landed yet, so that its parity wait passes a phase early.
 """
 import random
 
@@ -13,91 +14,108 @@ import pytest
 import protocol_model as pm
 
 
-def ring_model(segments, seed, W, S, mistake=None):
+def rings_model(segments, seed, W, depth, mistake=None):
     sim = pm.Sim(seed)
-    for s in range(S):
-        sim.bar(f"full{s}")
-        sim.bar(f"empty{s}")
-    stage = [None] * S
+    for w in range(W):
+        for s in range(depth):
+            sim.bar(f"full{w}.{s}")
     total = sum(segments)
-    met = [0] * len(segments)
-    eaten = []
+    stage = {(w, s): None for w in range(W) for s in range(depth)}
+    met, eaten = [0] * len(segments), []
 
-    def land(s, n):
+    def land(at, n):
         def put():
-            if stage[s] is not None:
-                raise pm.Hazard(f"tile {n} written over tile {stage[s]} in stage {s}")
-            stage[s] = n
+            if stage[at] is not None:
+                raise pm.Hazard(f"tile {n} written over tile {stage[at]}")
+            stage[at] = n
         return put
 
-    def producer():
-        for n in range(total):
-            s, k = n % S, n // S
-            if k > 0 and mistake != "no wait for the stage":
-                yield pm.wait(f"empty{s}", k - 1)
-            sim.tma.append((f"full{s}", land(s, n)))
-            yield pm.STEP
+    def warp(w):
+        mine = list(range(w, total, W))
+        issued = taken = base = 0
 
-    def consumer(w):
-        base = 0
+        def issue():
+            nonlocal issued
+            if issued < len(mine):
+                s = issued % depth
+                sim.tma.append((f"full{w}.{s}", land((w, s), mine[issued])))
+                issued += 1
+
+        for _ in range(depth):
+            issue()
+            yield pm.STEP
         for i, count in enumerate(segments):
-            n = base + (w + W - base % W) % W
-            while n < base + count:
-                s, k = n % S, n // S
-                yield pm.wait(f"full{s}", k)
-                if mistake == "released before it is read":
-                    sim.arrive(f"empty{s}")
-                    yield pm.STEP
-                if stage[s] != n:
-                    raise pm.Hazard(f"warp {w} read tile {stage[s]} for tile {n}")
+            while taken < len(mine) and mine[taken] < base + count:
+                s, phase = taken % depth, taken // depth
+                if mistake == "refilled before it is read":
+                    issue()
+                yield pm.wait(f"full{w}.{s}", phase + (mistake == "phase counted from one"))
+                if stage[w, s] != mine[taken]:
+                    raise pm.Hazard(f"warp {w} read tile {stage[w, s]} for tile {mine[taken]}")
                 yield pm.STEP
-                if stage[s] != n:
-                    raise pm.Hazard(f"tile {n} changed under warp {w}")
-                stage[s] = None
-                eaten.append(n)
-                if mistake != "released before it is read":
-                    sim.arrive(f"empty{s}")
-                n += W
+                stage[w, s] = None
+                eaten.append(mine[taken])
+                taken += 1
+                if mistake is None:
+                    issue()
             base += count
             met[i] += 1
             while met[i] < W:  # the warps' sums are joined here
                 yield pm.STEP
 
-    roles = {"producer": producer()}
-    roles.update({f"warp{w}": consumer(w) for w in range(W)})
-    sim.run(roles)
+    sim.run({f"warp{w}": warp(w) for w in range(W)})
     assert sorted(eaten) == list(range(total))
+
+
+def shared_ring_model(segments, seed, W, S):
+    """One ring for all warps, filled in order by a warp of its own."""
+    sim = pm.Sim(seed)
+    for s in range(S):
+        sim.bar(f"full{s}")
+        sim.bar(f"empty{s}")
+    total = sum(segments)
+
+    def producer():
+        for n in range(total):
+            if n >= S:
+                yield pm.wait(f"empty{n % S}", n // S - 1)
+            sim.tma.append((f"full{n % S}", lambda: None))
+            yield pm.STEP
+
+    def consumer(w):
+        for n in range(w, total, W):
+            yield pm.wait(f"full{n % S}", n // S)
+            yield pm.STEP
+            sim.arrive(f"empty{n % S}")
+
+    sim.run({"producer": producer(), **{f"warp{w}": consumer(w) for w in range(W)}})
 
 
 def segments_of(rng):
     return [rng.randrange(0, 30) for _ in range(rng.randrange(1, 5))]
 
 
-# (warps, stages) of the kernel's variants
-RINGS = [(6, 12), (5, 10), (4, 8), (4, 16), (8, 16), (8, 32), (7, 14), (7, 28)]
-
-
-@pytest.mark.parametrize("W,S", RINGS)
-def test_ring_is_safe(W, S):
-    rng = random.Random(W * 100 + S)
+@pytest.mark.parametrize("W,depth", [(4, 2), (4, 4), (5, 2), (6, 2), (6, 3), (8, 2), (8, 4), (12, 2)])
+def test_rings_are_safe(W, depth):
+    rng = random.Random(W * 100 + depth)
     for seed in range(150):
-        ring_model(segments_of(rng), seed, W, S)
+        rings_model(segments_of(rng), seed, W, depth)
 
 
-def _caught(W, S, mistake=None):
+def _caught(model, *args):
     for seed in range(400):
         try:
-            ring_model([20, 30], seed, W, S, mistake)
+            model([20, 30], seed, *args)
         except pm.Hazard:
             return True
     return False
 
 
-@pytest.mark.parametrize("mistake", ["no wait for the stage", "released before it is read"])
+@pytest.mark.parametrize("mistake", ["refilled before it is read", "phase counted from one", "never refilled"])
 def test_planted_mistake_is_caught(mistake):
-    assert _caught(6, 12, mistake)
+    assert _caught(rings_model, 6, 2, mistake)
 
 
 @pytest.mark.parametrize("W,S", [(8, 11), (7, 10), (4, 9)])
-def test_ring_that_changes_owners_is_caught(W, S):
-    assert _caught(W, S)
+def test_ring_whose_stages_change_owners_is_caught(W, S):
+    assert _caught(shared_ring_model, W, S)
