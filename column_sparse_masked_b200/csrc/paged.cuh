@@ -39,6 +39,16 @@ struct GatherParams {
   __nv_bfloat16 *k, *v;
 };
 
+// How the work is divided: equal runs of tiles per warp (items may be cut), whole items per warp, or one
+// CTA per item.
+enum PagedMode { kPagedSplit = 0, kPagedWhole = 1, kPagedCoop = 2 };
+
+// Warps of an attention CTA (one per SM).  Registers allow 7 at 255 a thread and 12 at 168; the rings of
+// tiles in shared memory allow 12 tiles of 16 KiB, 24 of 8.5 KiB.
+__host__ __device__ constexpr int paged_warps(int d, int bits, int rows) {
+  return bits == 16 ? (rows == 32 ? 4 : 6) : (rows == 32 ? 6 : rows == 16 ? 8 : 12);
+}
+
 struct PagedAttnParams {
   Pages pg;
   const __nv_bfloat16* q;
@@ -52,7 +62,7 @@ struct PagedAttnParams {
   // work: groups (a sequence, or a sequence and KV head with per-head masks) of `mult` items of `rows` rows
   int per_head, n_groups, mult, n_rb, rows, tile_keys;
   int min_tiles;            // units that a run holds at least
-  int uncut;                // one CTA per item, no parts
+  int mode;                 // kPaged*: how the work is divided
   // plan (with mask vectors): visible tiles of each group, row-visibility words of each key
   const int* counts;        // [n_groups]
   const int* list;          // [n_groups, list_stride]: tile << 1 | some pair hidden
@@ -61,10 +71,10 @@ struct PagedAttnParams {
   int n_words;
   int64_t words_stride;
   int words_shared;         // one word per key serves all rows
-  // partial sums of cut items: two slots per CTA
-  float* part;              // [2 grid, rows, d]
-  float2* stat;             // [2 grid, rows]: running maximum, sum
-  int* meta;                // [grid, 8]: the item that begins in a CTA's run and goes on in the next
+  // partial sums of cut items: two slots per run (worker: a warp)
+  float* part;              // [2 workers, rows, d]
+  float2* stat;             // [2 workers, rows]: running maximum, sum
+  int* meta;                // [workers, 8]: the item that begins in a run and goes on in the next
   uint64_t wait_limit_ns;
 };
 

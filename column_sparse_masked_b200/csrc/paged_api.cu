@@ -79,7 +79,7 @@ int check_paged_rows(const flashmask_pages* pg, const flashmask_paged_rows* r) {
 
 // Work split and workspace of an attention call.
 struct PagedLayout {
-  int per_head, n_groups, mult, n_rb, rows, tile_keys, n_words;
+  int per_head, n_groups, mult, n_rb, rows, tile_keys, n_words, mode;
   int64_t keys;  // capacity of the table, in whole tiles
   size_t part, stat, meta, counts, list, words, flags, bytes;
 };
@@ -99,16 +99,25 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
   L.keys = (cap + L.tile_keys - 1) / L.tile_keys * L.tile_keys;
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t o = off; off = ws_align(off + bytes); return o; };
-  L.part = take((size_t)2 * kPagedMaxCtas * L.rows * pg.d * 4);
-  L.stat = take((size_t)2 * kPagedMaxCtas * L.rows * 8);
-  L.meta = take((size_t)kPagedMaxCtas * 8 * 4);
+  // Whole items where cutting has nothing to give, and no second kernel: one per CTA if the device takes
+  // them all at once and the table bounds them to four tiles a warp, else one after another per warp if it
+  // bounds them to eight tiles.
+  const int64_t items = (int64_t)L.n_groups * L.mult, tiles = L.keys / L.tile_keys;
+  const int warps = paged_warps(pg.d, pg.bits, L.rows);
+  L.mode = items <= 128 && tiles <= 4 * warps ? kPagedCoop : tiles <= 8 ? kPagedWhole : kPagedSplit;
+  if (L.mode == kPagedSplit) {
+    const size_t slots = (size_t)2 * kPagedMaxCtas * warps;
+    L.part = take(slots * L.rows * pg.d * 4);
+    L.stat = take(slots * L.rows * 8);
+    L.meta = take(slots / 2 * 8 * 4);
+  }
   if (masked) {
     L.counts = take((size_t)L.n_groups * 4);
     L.list = take((size_t)L.n_groups * (L.keys / L.tile_keys) * 4);
     L.words = take((size_t)pg.B * r.Hm * L.n_words * L.keys * 4);
     L.flags = take((size_t)L.n_groups * (L.keys / L.tile_keys));
   }
-  L.bytes = off;
+  L.bytes = off > 0 ? off : 256;
   return L;
 }
 
@@ -228,11 +237,8 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
   p.n_rb = L.n_rb;
   p.rows = L.rows;
   p.tile_keys = L.tile_keys;
-  p.min_tiles = 8;
-  // One CTA per item, and no second kernel, where splitting has nothing to give: all items fit the device
-  // at once and the table itself bounds them to a few tiles per warp.
-  const int64_t items = (int64_t)L.n_groups * L.mult;
-  p.uncut = items <= di.sm_count && L.keys / L.tile_keys <= 16;
+  p.min_tiles = 2;
+  p.mode = L.mode;
   p.part = reinterpret_cast<float*>(ws + L.part);
   p.stat = reinterpret_cast<float2*>(ws + L.stat);
   p.meta = reinterpret_cast<int*>(ws + L.meta);
@@ -255,7 +261,7 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
     FM_TRY(make_rows_map(&tk, pages->k, rows, pages->d, box));
     FM_TRY(make_rows_map(&tv, pages->v, rows, pages->d, box));
   }
-  const int grid = p.uncut ? (int)items : persistent_grid(kPagedMaxCtas, di.sm_count);
+  const int grid = L.mode == kPagedCoop ? L.n_groups * L.mult : persistent_grid(kPagedMaxCtas, di.sm_count);
   FM_CUDA(launch_paged_attention(p, tk, tv, grid, plan, static_cast<cudaStream_t>(stream)));
   return FLASHMASK_OK;
 }

@@ -7,24 +7,25 @@
 //
 //  - Work.  An item is (sequence, KV head, block of 8, 16 or 32 rows); its
 //    units are its tiles of 32 or 64 keys.  All units are laid end to end and
-//    every CTA (one per SM) takes an equal run of them, whatever the lengths
+//    every warp of the device takes an equal run of them, whatever the lengths
 //    of the sequences: a run may end one item, hold several and begin another.
 //    An item inside one run is finished there; one that is cut leaves fp32
 //    partial sums, which a second kernel joins in a fixed order (no atomics:
 //    equal calls give equal bits).  Lengths are device data and the grid does
 //    not depend on them, so a captured graph serves growing sequences.
+//  - Warps work alone: each looks its pages up, fills a ring of tiles of its
+//    own in shared memory by TMA (swizzled boxes for bf16, plain bulk copies
+//    for 4 bits) and keeps its own running maximum and sums; the ring runs on
+//    into the next item, so the loads never pause at an item's end.
+//  - Few short items (a table of a few tiles per warp) take one CTA each
+//    instead, whose warps share the tiles and join their sums in shared memory.
 //  - Masks.  With mask vectors a plan kernel runs first: it turns each key's
 //    four boundaries into one bit per row, and lists the tiles that some row
 //    sees, so hidden tiles are neither read nor counted as work.
-//  - Loads.  One warp looks pages up and fills a ring of tiles in shared
-//    memory by TMA (swizzled boxes for bf16, plain bulk copies for 4 bits);
-//    the ring spans items, so the loads never pause at an item's end.
 //  - Products.  Tensor cores with the keys as the M side (mma m16n8k16): S^T =
 //    K Q^T and O^T = V^T P^T need only 8 row columns, where the usual
 //    orientation pads the rows to 16.  mma.sync and not tcgen05: rows are
 //    few, P never leaves registers, and the tensor pipe is far from the bound.
-//    Each warp keeps its own running maximum and sums over its tiles; warps
-//    meet once per item.
 //  - 4 bits.  A row's codes enter the products as the integers code - 8 (exact
 //    in bf16); scale and minimum are applied to sums in fp32:
 //      q.k = s (q.(c - 8)) + (m + 8 s) sum(q)
@@ -32,6 +33,8 @@
 //    The contraction may run over the head's values in any order as long as
 //    both sides agree, so each thread takes whole 16-byte pieces of code rows.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "launchers.h"
 #include "paged.cuh"
@@ -65,14 +68,14 @@ __device__ __forceinline__ int tiles_of(const PagedAttnParams& p, int g) {
   return (key_bound(p, group_batch(p, g), &len, &st) + p.tile_keys - 1) / p.tile_keys;
 }
 
-// A run of units, walked segment by segment (a segment: tiles [t, t + n) of
-// one item).  Every warp of the CTA walks it the same way.
+// A run, walked segment by segment (a segment: tiles [t, t + n) of one item).
+// Runs are made of units (tiles), or of whole items.
 struct Walk {
   int g, in, t, T;  // group, item in the group, first tile, tiles of the group's items
-  int left;         // units left in the run
+  int left;         // units (items) left in the run
   int n;            // tiles of this segment
   __device__ __forceinline__ bool next(const PagedAttnParams& p) {
-    left -= n;
+    left -= p.mode == kPagedSplit ? n : 1;
     if (left <= 0) return false;
     t = 0;
     if (++in == p.mult) {
@@ -80,11 +83,16 @@ struct Walk {
       do {
         ++g;
         T = tiles_of(p, g);
-      } while (T == 0);
+      } while (T == 0 && p.mode == kPagedSplit);
     }
-    n = min(T, left);
+    n = p.mode == kPagedSplit ? min(T, left) : T;
     return true;
   }
+};
+
+// A warp's run of units: [u0, u0 + ...), one of runs of q units, one more for the first rem.
+struct Run {
+  int worker, u0, q, rem;
 };
 
 struct Item {
@@ -106,7 +114,7 @@ template <int D, int BITS, int NT>
 struct Cfg {
   static constexpr int kKT = BITS == 16 && D == 128 ? 32 : 64;  // keys of a tile
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = BITS == 16 ? (NT == 4 ? 4 : NT == 2 ? 5 : 6) : (NT == 4 ? 4 : NT == 2 ? 7 : 8);
+  static constexpr int kWarps = paged_warps(D, BITS, kRows);
   static constexpr int kThreads = 32 * kWarps;
   static constexpr bool kQShared = NT == 4;                     // Q fragments in shared memory
   static constexpr int kRowBytes = BITS == 16 ? 2 * D : D / 2;
@@ -114,43 +122,42 @@ struct Cfg {
   static constexpr int kScales = BITS == 4 ? kKT * 4 : 0;
   static constexpr int kStage = 2 * kHalf + 2 * kScales;
   static constexpr int kStride = D + 4;                         // floats between rows of the merge buffer
-  static constexpr int kMerge = kWarps * kRows * kStride * 4;
-  static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
+  static constexpr int kMerge = kWarps * kRows * kStride * 4;   // on top of the rings
+  static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;  // per warp
   static constexpr int kPerStage = kStage + 16 + 8;             // + header, barrier
-  static constexpr int kFixed = kMerge + kQBytes + 3 * kWarps * kRows * 4 + kRows * 4 + 1024 + 256;
+  static constexpr int kFixed = kWarps * (kQBytes + 4 * kRows * 4) + 1024 + 256;
   // Every warp has a ring of its own, which it fills and empties itself: a stage is refilled by the warp
-  // that has just read it, so nothing waits for another warp between the ends of items.
+  // that has just read it, so nothing waits for another warp.
   static constexpr int kFit = (225 * 1024 - kFixed) / kPerStage / kWarps;
   static constexpr int kDepth = kFit > 4 ? 4 : kFit;
   static constexpr int kStages = kWarps * kDepth;
   static constexpr int kSmem = kFixed + kStages * kPerStage;
   static constexpr int kBoxes = kKT / 16;                       // copies of a tile's rows at most
   static_assert(kDepth >= 2, "ring too short");
+  static_assert(kMerge <= kStages * kStage, "the merge buffer lies on the rings");
 };
 
 template <int D, int BITS, int NT>
 struct Smem {
   using C = Cfg<D, BITS, NT>;
-  uint8_t* stage;      // kStages x kStage, 1024-byte aligned for the swizzle
+  uint8_t* stage;      // kStages x kStage, 1024-byte aligned for the swizzle; kDepth in a row per warp
   int4* hdr;           // kStages: first key, some pair hidden, valid boxes
   uint64_t* full;      // kStages
-  float* merge;        // kWarps x kRows x kStride
-  uint2* q;            // Q fragments (kQShared)
-  float *m, *l, *c;    // kWarps x kRows
-  float* qsum;         // kRows
+  uint2* q;            // Q fragments of each warp (kQShared)
+  float *m, *l, *c;    // kWarps x kRows (one item per CTA)
+  float* qsum;         // kWarps x kRows
   int* abort;
   __device__ __forceinline__ explicit Smem(uint8_t* raw) {
     const uint32_t a = smem_addr(raw);
     uint8_t* x = raw + ((1024u - (a & 1023u)) & 1023u);
     stage = x; x += C::kStages * C::kStage;
-    merge = reinterpret_cast<float*>(x); x += C::kMerge;
-    q = reinterpret_cast<uint2*>(x); x += C::kQBytes;
+    q = reinterpret_cast<uint2*>(x); x += C::kWarps * C::kQBytes;
     hdr = reinterpret_cast<int4*>(x); x += C::kStages * 16;
     full = reinterpret_cast<uint64_t*>(x); x += C::kStages * 8;
     m = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
     l = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
     c = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
-    qsum = reinterpret_cast<float*>(x); x += C::kRows * 4;
+    qsum = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
     abort = reinterpret_cast<int*>(x);
   }
 };
@@ -213,10 +220,10 @@ __device__ __forceinline__ float sum8(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-// Fills one warp's ring: the tiles of the CTA's run that are the warp's, in
-// order, across segments.  Pages are looked up for 32 of them at a time, one
-// by each lane.
-template <int D, int BITS, int NT>
+// Fills one warp's ring with the warp's tiles of the run, in order, across
+// segments: every STEP-th tile from the first one on.  Pages are looked up
+// for 32 of them at a time, one by each lane.
+template <int D, int BITS, int NT, int STEP>
 struct Issuer {
   using C = Cfg<D, BITS, NT>;
   Walk w;
@@ -227,23 +234,22 @@ struct Issuer {
   int kvh;
   int j0, flags, page[C::kBoxes];  // a lane's tile: first key, masked | valid boxes << 1, pages
 
-  __device__ __forceinline__ void batch(const PagedAttnParams& p) {
+  __device__ __forceinline__ void batch(const PagedAttnParams& p, int box_shift) {
     constexpr int KT = C::kKT;
-    const int lane = threadIdx.x & 31, box_shift = min(p.pg.page_shift, KT == 32 ? 5 : 6);
-    const int boxes = KT >> box_shift;
+    const int lane = threadIdx.x & 31, boxes = KT >> box_shift;
     const Item it = item_of(p, w.g, w.in, C::kRows);
     kvh = it.kvh;
     int len;
     int64_t first;
     const int hi = key_bound(p, it.b, &len, &first);
-    nb = min(32, (w.n - k + C::kWarps - 1) / C::kWarps);
+    nb = min(32, (w.n - k + STEP - 1) / STEP);
     x = 0;
     j0 = 0;
     int masked = 0, valid = 0;
 #pragma unroll
     for (int i = 0; i < C::kBoxes; ++i) page[i] = 0;
     if (lane < nb) {
-      const int t = w.t + k + lane * C::kWarps;
+      const int t = w.t + k + lane * STEP;
       if (p.list) {
         const int e = p.list[(int64_t)w.g * p.list_stride + t];
         j0 = (e >> 1) * KT;
@@ -265,19 +271,19 @@ struct Issuer {
       if (valid != (1 << boxes) - 1) masked = 1;
     }
     flags = masked | (valid << 1);
-    k += nb * C::kWarps;
+    k += nb * STEP;
   }
 
-  __device__ __forceinline__ void start(const PagedAttnParams& p, const Walk& wk, int warp) {
+  __device__ __forceinline__ void start(const Walk& wk, int first_tile) {
     w = wk;
-    k = warp;
+    k = first_tile;
     issued = 0;
     x = nb = 0;
     more = true;
   }
 
   __device__ __forceinline__ void issue(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
-                                        const Smem<D, BITS, NT>& sm, int warp) {
+                                        const Smem<D, BITS, NT>& sm, int warp, int box_shift) {
     if (x == nb) {
       if (!more) return;
       while (k >= w.n) {
@@ -288,60 +294,63 @@ struct Issuer {
           return;
         }
       }
-      batch(p);
+      batch(p, box_shift);
     }
-    constexpr int KT = C::kKT;
-    const int lane = threadIdx.x & 31, box_shift = min(p.pg.page_shift, KT == 32 ? 5 : 6);
+    const int lane = threadIdx.x & 31;
     const int tj = __shfl_sync(0xffffffffu, j0, x), f = __shfl_sync(0xffffffffu, flags, x);
-    const int bx = BITS == 16 ? lane >> 1 : lane >> 2;  // a copy per lane
-    int pid = 0;
-#pragma unroll
-    for (int i = 0; i < C::kBoxes; ++i) {
-      const int v = __shfl_sync(0xffffffffu, page[i], x);
-      if (i == bx) pid = v;
-    }
-    ++x;
     const int stage = warp * C::kDepth + issued % C::kDepth;
-    ++issued;
     uint64_t* bar = &sm.full[stage];
+    uint8_t* st = sm.stage + stage * C::kStage;
     if (lane == 0) {
       sm.hdr[stage] = make_int4(tj, f & 1, f >> 1, 0);
       mbar_arrive_expect_tx(bar, (uint32_t)(__popc(f >> 1) << box_shift) * (2 * C::kRowBytes + (BITS == 4 ? 8 : 0)));
     }
-    __syncwarp();
-    if (bx < C::kBoxes && ((f >> (1 + bx)) & 1)) {
-      const int64_t row = row_of(p.pg, pid, kvh, tj + (bx << box_shift));
-      uint8_t* st = sm.stage + stage * C::kStage;
-      if (BITS == 16) {
-        tma_load_rows(st + (lane & 1) * C::kHalf + (bx << box_shift) * C::kRowBytes, (lane & 1) ? tv : tk, bar,
-                      (int)row);
-      } else {
-        const int part = lane & 3;  // K codes, V codes, K scales, V scales
-        const uint8_t* src = part == 0 ? p.pg.k : part == 1 ? p.pg.v
-                             : reinterpret_cast<const uint8_t*>(part == 2 ? p.pg.k_scales : p.pg.v_scales);
-        const int rb = part < 2 ? C::kRowBytes : 4;
-        const int at = (part & 1) * (part < 2 ? C::kHalf : C::kScales) + (part < 2 ? 0 : 2 * C::kHalf);
-        bulk_load(st + at + (bx << box_shift) * rb, src + row * rb, (uint32_t)rb << box_shift, bar);
+#pragma unroll
+    for (int i = 0; i < C::kBoxes; ++i) {
+      if (i >= (C::kKT >> box_shift)) break;
+      const int pid = __shfl_sync(0xffffffffu, page[i], x);
+      if (lane == 0 && ((f >> (1 + i)) & 1)) {
+        const int64_t row = row_of(p.pg, pid, kvh, tj + (i << box_shift));
+        if (BITS == 16) {
+          uint8_t* dst = st + (i << box_shift) * C::kRowBytes;
+          tma_load_rows(dst, tk, bar, (int)row);
+          tma_load_rows(dst + C::kHalf, tv, bar, (int)row);
+        } else {
+          const uint32_t bytes = (uint32_t)C::kRowBytes << box_shift;
+          uint8_t* dst = st + (i << box_shift) * C::kRowBytes;
+          bulk_load(dst, p.pg.k + row * C::kRowBytes, bytes, bar);
+          bulk_load(dst + C::kHalf, p.pg.v + row * C::kRowBytes, bytes, bar);
+          uint8_t* sc = st + 2 * C::kHalf + (i << box_shift) * 4;
+          bulk_load(sc, p.pg.k_scales + row, 4u << box_shift, bar);
+          bulk_load(sc + C::kScales, p.pg.v_scales + row, 4u << box_shift, bar);
+        }
       }
     }
+    ++x;
+    ++issued;
   }
 };
 
-template <int D, int BITS, int NT>
+// One warp's run (COOP: its share of the CTA's item): scores, softmax and
+// values of every tile, and the item's rows or its partial sums at the end of
+// each segment.
+template <int D, int BITS, int NT, bool COOP>
 __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
-                                       const Smem<D, BITS, NT>& sm, Walk wk, const WaitCtx& wc) {
+                                       const Smem<D, BITS, NT>& sm, Walk wk, const WaitCtx& wc, const Run& run) {
   using C = Cfg<D, BITS, NT>;
   constexpr int KT = C::kKT, MT = D / 16, KS = D / 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, q4 = lane & 3;  // the fragment's row in a block of 8, and its column pair
   const int box_shift = min(p.pg.page_shift, KT == 32 ? 5 : 6);
   const uint32_t box_rows = 1u << box_shift;
-  Issuer<D, BITS, NT> is;
-  is.start(p, wk, warp);
+  constexpr int STEP = COOP ? C::kWarps : 1;
+  Issuer<D, BITS, NT, STEP> is;
+  is.start(wk, COOP ? warp : 0);
 #pragma unroll 1
-  for (int i = 0; i < C::kDepth; ++i) is.issue(p, tk, tv, sm, warp);
-  int k = warp, taken = 0;  // the warp's next tile in the segment, and the tiles it has taken
+  for (int i = 0; i < C::kDepth; ++i) is.issue(p, tk, tv, sm, warp, box_shift);
+  int k = COOP ? warp : 0, taken = 0;  // the warp's next tile in the segment, and the tiles it has taken
   bool alive = true, first_seg = true;
+  int u = run.u0;  // first unit of the segment
   do {
     const Item it = item_of(p, wk.g, wk.in, C::kRows);
     int len;
@@ -390,25 +399,28 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
         }
       }
     } else {
-      for (int x = warp; x < KS * NT; x += C::kWarps) sm.q[x * 32 + lane] = load_q(x / NT, x % NT);
-      if (BITS == 4 && warp == 0) {
+      uint2* qw = sm.q + warp * (C::kQBytes / 8);
+#pragma unroll 4
+      for (int x = 0; x < KS * NT; ++x) qw[x * 32 + lane] = load_q(x / NT, x % NT);
+      if (BITS == 4) {
         float s = 0.f;
         if (lane < C::kRows && lane < R) {
           const int row = it.row0 + lane, i = row / p.G, h = it.kvh * p.G + row % p.G;
           const __nv_bfloat16* src = qb + i * p.qs[1] + h * p.qs[2];
           for (int x = 0; x < D; ++x) s += __bfloat162float(src[x]);
         }
-        if (lane < C::kRows) sm.qsum[lane] = s;
+        if (lane < C::kRows) sm.qsum[warp * C::kRows + lane] = s;
       }
-      __syncthreads();
+      __syncwarp();
       if (BITS == 4) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          qsum[2 * nt] = sm.qsum[nt * 8 + 2 * q4];
-          qsum[2 * nt + 1] = sm.qsum[nt * 8 + 2 * q4 + 1];
+          qsum[2 * nt] = sm.qsum[warp * C::kRows + nt * 8 + 2 * q4];
+          qsum[2 * nt + 1] = sm.qsum[warp * C::kRows + nt * 8 + 2 * q4 + 1];
         }
       }
     }
+    const uint2* qw = sm.q + warp * (C::kQBytes / 8);
 
     float acc[MT][NT][4], mx[2 * NT], sum[2 * NT], cor[2 * NT];
 #pragma unroll
@@ -424,11 +436,11 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
 
-    for (; k < wk.n; k += C::kWarps) {
+    for (; k < wk.n; k += STEP) {
       const int stage = warp * C::kDepth + taken % C::kDepth;
       if (alive) alive = mbar_wait(&sm.full[stage], (taken / C::kDepth) & 1u, wc);
       alive = __all_sync(0xffffffffu, alive);
-      if (!alive) continue;  // keeps walking: the barriers at the ends of segments are still met
+      if (!alive) continue;
       ++taken;
       const int4 hd = sm.hdr[stage];
       uint8_t* st = sm.stage + stage * C::kStage;
@@ -462,7 +474,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
               ldsm4(a, kaddr + block16(sb + m2 * 16) + (ks >> 2) * (box_rows * 128) + lrow + (((ch & 7) ^ (lane & 7)) << 4));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const uint2 b = C::kQShared ? sm.q[(ks * NT + nt) * 32 + lane] : qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
+                const uint2 b = C::kQShared ? qw[(ks * NT + nt) * 32 + lane] : qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
                 mma16816(s[m2][nt], a, b.x, b.y);
               }
             }
@@ -487,7 +499,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
                                      centred(r1[ks >> 1], i + 1)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const uint2 b = C::kQShared ? sm.q[(ks * NT + nt) * 32 + lane] : qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
+                const uint2 b = C::kQShared ? qw[(ks * NT + nt) * 32 + lane] : qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
                 mma16816(s[m2][nt], a, b.x, b.y);
               }
             }
@@ -701,89 +713,152 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
       }
       if (wrote) fence_async_smem();
       __syncwarp();
-      is.issue(p, tk, tv, sm, warp);
+      is.issue(p, tk, tv, sm, warp, box_shift);
     }
     k -= wk.n;
 
-    // ---- the warps' sums together ----
 #pragma unroll
     for (int x = 0; x < 2 * NT; ++x) {
       sum[x] = sum8(sum[x]);
       if (BITS == 4) cor[x] = sum8(cor[x]);
     }
-    if (g8 == 0) {
+    if (COOP) {
+      // ---- the warps' sums together; the rings are empty and hold them ----
+      if (g8 == 0) {
 #pragma unroll
-      for (int x = 0; x < 2 * NT; ++x) {
-        const int r = warp * C::kRows + (x >> 1) * 8 + 2 * q4 + (x & 1);
-        sm.m[r] = mx[x];
-        sm.l[r] = sum[x];
-        if (BITS == 4) sm.c[r] = cor[x];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < 2 * NT; ++x) {
-      const int r = (x >> 1) * 8 + 2 * q4 + (x & 1);
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, sm.m[w * C::kRows + r]);
-      const float f = mx[x] == -INFINITY ? 0.f : fast_exp2((mx[x] - top) * p.scale_log2);
-      float* dst = sm.merge + (warp * C::kRows + r) * C::kStride;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (BITS == 16) {
-          dst[mt * 16 + g8] = acc[mt][x >> 1][x & 1] * f;
-          dst[mt * 16 + 8 + g8] = acc[mt][x >> 1][2 + (x & 1)] * f;
-        } else {
-          *reinterpret_cast<float2*>(dst + g8 * (D / 8) + 2 * mt) =
-              make_float2(acc[mt][x >> 1][x & 1] * f, acc[mt][x >> 1][2 + (x & 1)] * f);
+        for (int x = 0; x < 2 * NT; ++x) {
+          const int r = warp * C::kRows + (x >> 1) * 8 + 2 * q4 + (x & 1);
+          sm.m[r] = mx[x];
+          sm.l[r] = sum[x];
+          if (BITS == 4) sm.c[r] = cor[x];
         }
       }
-    }
-    __syncthreads();
-    const bool whole = wk.n == wk.T;
-    const int slot = 2 * blockIdx.x + (first_seg ? 0 : 1);
-    for (int x = threadIdx.x; x < C::kRows * (D / 4); x += 32 * C::kWarps) {
-      const int r = x / (D / 4), d4 = x % (D / 4);
-      if (r >= R) continue;
-      float top = -INFINITY, L = 0.f, cc = 0.f;
+      __syncthreads();
+      float* merge = reinterpret_cast<float*>(sm.stage);
 #pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, sm.m[w * C::kRows + r]);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x = 0; x < 2 * NT; ++x) {
+        const int r = (x >> 1) * 8 + 2 * q4 + (x & 1);
+        float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) {
-        const float m = sm.m[w * C::kRows + r];
-        const float f = m == -INFINITY ? 0.f : fast_exp2((m - top) * p.scale_log2);
-        L = fmaf(sm.l[w * C::kRows + r], f, L);
-        if (BITS == 4) cc = fmaf(sm.c[w * C::kRows + r], f, cc);
-        const float4 v = *reinterpret_cast<const float4*>(sm.merge + (w * C::kRows + r) * C::kStride + 4 * d4);
-        o.x += v.x;
-        o.y += v.y;
-        o.z += v.z;
-        o.w += v.w;
+        for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, sm.m[w * C::kRows + r]);
+        const float f = mx[x] == -INFINITY ? 0.f : fast_exp2((mx[x] - top) * p.scale_log2);
+        float* dst = merge + (warp * C::kRows + r) * C::kStride;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          if (BITS == 16) {
+            dst[mt * 16 + g8] = acc[mt][x >> 1][x & 1] * f;
+            dst[mt * 16 + 8 + g8] = acc[mt][x >> 1][2 + (x & 1)] * f;
+          } else {
+            *reinterpret_cast<float2*>(dst + g8 * (D / 8) + 2 * mt) =
+                make_float2(acc[mt][x >> 1][x & 1] * f, acc[mt][x >> 1][2 + (x & 1)] * f);
+          }
+        }
       }
-      if (BITS == 4) {
-        o.x += cc;
-        o.y += cc;
-        o.z += cc;
-        o.w += cc;
-      }
-      if (whole) {
+      __syncthreads();
+      for (int x = threadIdx.x; x < min(C::kRows, R) * (D / 4); x += 32 * C::kWarps) {
+        const int r = x / (D / 4), d4 = x % (D / 4);
+        float top = -INFINITY, L = 0.f, cc = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, sm.m[w * C::kRows + r]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::kWarps; ++w) {
+          const float m = sm.m[w * C::kRows + r];
+          const float f = m == -INFINITY ? 0.f : fast_exp2((m - top) * p.scale_log2);
+          L = fmaf(sm.l[w * C::kRows + r], f, L);
+          if (BITS == 4) cc = fmaf(sm.c[w * C::kRows + r], f, cc);
+          const float4 v = *reinterpret_cast<const float4*>(merge + (w * C::kRows + r) * C::kStride + 4 * d4);
+          o.x += v.x;
+          o.y += v.y;
+          o.z += v.z;
+          o.w += v.w;
+        }
         const int row = it.row0 + r, i = row / p.G, h = it.kvh * p.G + row % p.G;
         const float inv = top == -INFINITY ? 0.f : 1.f / L;
-        const int64_t at = (((int64_t)it.b * p.Nq + i) * p.Hq + h) * D + 4 * d4;
-        *reinterpret_cast<uint2*>(p.o + at) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2*>(p.o + (((int64_t)it.b * p.Nq + i) * p.Hq + h) * D + 4 * d4) =
+            make_uint2(pack_bf16x2((o.x + cc) * inv, (o.y + cc) * inv), pack_bf16x2((o.z + cc) * inv, (o.w + cc) * inv));
         if (d4 == 0)
           p.lse[((int64_t)it.b * p.Hq + h) * p.Nq + i] =
               top == -INFINITY ? -INFINITY : fmaf(top, p.scale_log2, log2f(L)) * kLn2;
-      } else {
-        *reinterpret_cast<float4*>(p.part + (slot * C::kRows + r) * D + 4 * d4) = o;
-        if (d4 == 0) p.stat[slot * C::kRows + r] = make_float2(top, L);
+      }
+    } else if (wk.n == wk.T) {
+      // ---- the whole item: its rows ----
+#pragma unroll
+      for (int x = 0; x < 2 * NT; ++x) {
+        const float inv = mx[x] == -INFINITY ? 0.f : 1.f / sum[x];
+        const int r = (x >> 1) * 8 + 2 * q4 + (x & 1), row = it.row0 + r, i = row / p.G;
+        if (g8 == 0 && r < R)
+          p.lse[((int64_t)it.b * p.Hq + it.kvh * p.G + row % p.G) * p.Nq + i] =
+              mx[x] == -INFINITY ? -INFINITY : fmaf(mx[x], p.scale_log2, log2f(sum[x])) * kLn2;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          acc[mt][x >> 1][x & 1] = (acc[mt][x >> 1][x & 1] + cor[x]) * inv;
+          acc[mt][x >> 1][2 + (x & 1)] = (acc[mt][x >> 1][2 + (x & 1)] + cor[x]) * inv;
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (BITS == 16) {  // 8 x 8 blocks turned, so that a lane has neighbouring values of one row
+          const int r = nt * 8 + g8, row = it.row0 + r, i = row / p.G;
+          __nv_bfloat16* dst = p.o + (((int64_t)it.b * p.Nq + i) * p.Hq + it.kvh * p.G + row % p.G) * D + 2 * q4;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t v = transpose8x8(pack_bf16x2(acc[mt][nt][2 * u], acc[mt][nt][2 * u + 1]));
+              if (r < R) *reinterpret_cast<uint32_t*>(dst + mt * 16 + u * 8) = v;
+            }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = nt * 8 + 2 * q4 + e, row = it.row0 + r, i = row / p.G;
+            if (r >= R) continue;
+            __nv_bfloat16* dst = p.o + (((int64_t)it.b * p.Nq + i) * p.Hq + it.kvh * p.G + row % p.G) * D + g8 * (D / 8);
+#pragma unroll
+            for (int mt = 0; mt < MT; mt += 4)
+              *reinterpret_cast<uint4*>(dst + 2 * mt) =
+                  make_uint4(pack_bf16x2(acc[mt][nt][e], acc[mt][nt][2 + e]),
+                             pack_bf16x2(acc[mt + 1][nt][e], acc[mt + 1][nt][2 + e]),
+                             pack_bf16x2(acc[mt + 2][nt][e], acc[mt + 2][nt][2 + e]),
+                             pack_bf16x2(acc[mt + 3][nt][e], acc[mt + 3][nt][2 + e]));
+          }
+        }
+      }
+    } else {
+      // ---- part of an item: sums and running maximum ----
+      const int slot = 2 * run.worker + (first_seg ? 0 : 1);
+      if (wk.t == 0 && lane == 0) {  // it begins here and goes on in the next runs: where its parts are
+        const int last = u + wk.T - 1, big = run.rem * (run.q + 1);  // the run that ends it holds unit `last`
+        int* meta = p.meta + run.worker * kMetaInts;
+        meta[0] = it.b;
+        meta[1] = it.kvh;
+        meta[2] = it.row0;
+        meta[3] = last < big ? last / (run.q + 1) : run.rem + (last - big) / run.q;
+        meta[4] = first_seg ? 0 : 1;
+      }
+#pragma unroll
+      for (int x = 0; x < 2 * NT; ++x) {
+        const int r = (x >> 1) * 8 + 2 * q4 + (x & 1);
+        if (r >= R) continue;
+        if (g8 == 0) p.stat[slot * C::kRows + r] = make_float2(mx[x], sum[x]);
+        float* dst = p.part + ((int64_t)slot * C::kRows + r) * D;
+        if (BITS == 16) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            dst[mt * 16 + g8] = acc[mt][x >> 1][x & 1];
+            dst[mt * 16 + 8 + g8] = acc[mt][x >> 1][2 + (x & 1)];
+          }
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < MT; mt += 2)
+            *reinterpret_cast<float4*>(dst + g8 * (D / 8) + 2 * mt) =
+                make_float4(acc[mt][x >> 1][x & 1] + cor[x], acc[mt][x >> 1][2 + (x & 1)] + cor[x],
+                            acc[mt + 1][x >> 1][x & 1] + cor[x], acc[mt + 1][x >> 1][2 + (x & 1)] + cor[x]);
+        }
       }
     }
-    __syncthreads();
     first_seg = false;
+    u += wk.n;
   } while (wk.next(p));
   if (!alive && lane == 0) {  // gave up: let the copies in flight land before the CTA ends
     WaitCtx w2 = wc;
@@ -794,22 +869,18 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
   }
 }
 
-// Rows of a group (items in0 <= item < in1 of it) whose keys are all hidden or missing.
+// Rows of a group whose keys are all hidden or missing.
 template <int D>
-__device__ void write_empty(const PagedAttnParams& p, int g, int in0, int in1, int threads) {
-  const int b = group_batch(p, g), R = p.Nq * p.G;
-  for (int in = in0; in < in1; ++in) {
-    const Item it = item_of(p, g, in, p.rows);
-    const int n = min(p.rows, R - it.row0);
-    for (int x = threadIdx.x; x < n * (D / 8); x += threads) {
-      const int row = it.row0 + x / (D / 8), c = x % (D / 8), i = row / p.G, h = it.kvh * p.G + row % p.G;
-      *reinterpret_cast<uint4*>(p.o + (((int64_t)b * p.Nq + i) * p.Hq + h) * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
-      if (c == 0) p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] = -INFINITY;
-    }
+__device__ void write_empty(const PagedAttnParams& p, int g, int threads) {
+  const int b = group_batch(p, g), heads = p.per_head ? p.G : p.Hq, h0 = p.per_head ? (g % p.pg.Hkv) * p.G : 0;
+  for (int64_t x = threadIdx.x; x < (int64_t)p.Nq * heads * (D / 8); x += threads) {
+    const int c = (int)(x % (D / 8)), h = h0 + (int)(x / (D / 8) % heads), i = (int)(x / (D / 8) / heads);
+    *reinterpret_cast<uint4*>(p.o + (((int64_t)b * p.Nq + i) * p.Hq + h) * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+    if (c == 0) p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] = -INFINITY;
   }
 }
 
-template <int D, int BITS, int NT>
+template <int D, int BITS, int NT, bool COOP>
 __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                            const __grid_constant__ PagedAttnParams p) {
@@ -832,18 +903,32 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  if (p.uncut) {  // one item per CTA
-    Walk wk;
+  Walk wk;
+  if (COOP) {  // one item per CTA
     wk.g = blockIdx.x / p.mult;
     wk.in = blockIdx.x % p.mult;
     wk.t = 0;
-    wk.T = wk.n = wk.left = tiles_of(p, wk.g);
-    if (wk.T == 0) write_empty<D>(p, wk.g, wk.in, wk.in + 1, C::kThreads);
-    else attend<D, BITS, NT>(p, &tk, &tv, sm, wk, wc);
+    wk.T = wk.n = tiles_of(p, wk.g);
+    wk.left = 1;
+    attend<D, BITS, NT, true>(p, &tk, &tv, sm, wk, wc, Run{});
+    return;
+  }
+  // neighbouring runs go to different SMs: a small problem's few runs are spread over the device
+  const int worker = warp * gridDim.x + blockIdx.x, all_workers = C::kWarps * gridDim.x;
+  if (p.mode == kPagedWhole) {
+    const int items = p.n_groups * p.mult, q = items / all_workers, rem = items - q * all_workers;
+    const int first = worker * q + min(worker, rem);
+    wk.left = q + (worker < rem ? 1 : 0);
+    if (wk.left == 0) return;
+    wk.g = first / p.mult;
+    wk.in = first % p.mult;
+    wk.t = 0;
+    wk.T = wk.n = tiles_of(p, wk.g);
+    attend<D, BITS, NT, false>(p, &tk, &tv, sm, wk, wc, Run{});
     return;
   }
 
-  // ---- this CTA's run of units: every warp sums the groups' tiles and finds the group it begins in ----
+  // ---- every warp sums the groups' tiles and finds the group that its run begins in ----
   const int per = (p.n_groups + 31) / 32, ga = min(lane * per, p.n_groups), gb = min(ga + per, p.n_groups);
   int mine = 0;
 #pragma unroll 4
@@ -855,14 +940,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
     if (lane >= o) incl += x;
   }
   const int total = __shfl_sync(0xffffffffu, incl, 31) * p.mult;
-  // units of a run: total / ctas, one more for the first total % ctas
-  const int ctas = min((int)gridDim.x, max(1, total / p.min_tiles)), q = total / ctas, rem = total - q * ctas;
-  const int c = blockIdx.x;
-  const int u0 = c * q + min(c, rem), n_units = c < ctas ? q + (c < rem ? 1 : 0) : 0;
+  // units of a run: total / workers, one more for the first total % workers
+  const int workers = min(all_workers, max(1, total / p.min_tiles)), q = total / workers, rem = total - q * workers;
+  const int u0 = worker * q + min(worker, rem), n_units = worker < workers ? q + (worker < rem ? 1 : 0) : 0;
+  if (lane == 0) p.meta[worker * kMetaInts] = -1;
   if (n_units > 0) {
     const unsigned has = __ballot_sync(0xffffffffu, u0 < incl * p.mult);
     const int src = __ffs(has) - 1;
-    Walk wk;
     int at = (incl - mine) * p.mult;
     wk.g = ga;
     wk.T = 0;
@@ -880,102 +964,132 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
     wk.t = off - wk.in * wk.T;
     wk.left = n_units;
     wk.n = min(wk.T - wk.t, n_units);
-    attend<D, BITS, NT>(p, &tk, &tv, sm, wk, wc);
-
-    // an item that begins in this run and goes on in the next ones: where its parts are
-    if (tid == 0) {
-      int* meta = p.meta + c * kMetaInts;
-      bool first = true;
-      int u = u0;
-      while (u + wk.n < u0 + n_units) {
-        u += wk.n;
-        first = false;
-        wk.next(p);
-      }
-      meta[0] = -1;
-      if (wk.t == 0 && wk.n < wk.T) {
-        const Item it = item_of(p, wk.g, wk.in, C::kRows);
-        const int last = u + wk.T - 1, big = rem * (q + 1);  // the CTA that ends it holds unit `last`
-        meta[0] = it.b;
-        meta[1] = it.kvh;
-        meta[2] = it.row0;
-        meta[3] = last < big ? last / (q + 1) : rem + (last - big) / q;
-        meta[4] = first ? 0 : 1;
-      }
-    }
-  } else if (tid == 0) {
-    p.meta[c * kMetaInts] = -1;
+    attend<D, BITS, NT, false>(p, &tk, &tv, sm, wk, wc, Run{worker, u0, q, rem});
   }
-  for (int g = c; g < p.n_groups; g += gridDim.x)
-    if (tiles_of(p, g) == 0) write_empty<D>(p, g, 0, p.mult, C::kThreads);
+  for (int g = blockIdx.x; g < p.n_groups; g += gridDim.x)
+    if (tiles_of(p, g) == 0) write_empty<D>(p, g, C::kThreads);
 }
 
 // ---------------------------------------------------------------------------
-// joining the parts of cut items: one CTA per (run, row)
+// joining the parts of cut items: a warp per run and row where they are few,
+// the CTA together where they are many
 // ---------------------------------------------------------------------------
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
-  constexpr int LG = D / 4, NGR = 256 / LG;
-  __shared__ float w[256], red[8];
-  __shared__ float4 buf[NGR][LG];
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int workers) {
+  constexpr int LG = D / 4, PP = 32 / LG;  // lanes of a row, parts that a warp reads at a time
+  __shared__ float red[8], wts[256];
+  __shared__ float4 buf[8][32];
   griddep_wait();
-  const int* meta = p.meta + blockIdx.x * kMetaInts;
-  const int b = meta[0];
-  if (b < 0) return;
-  const int r = blockIdx.y, row = meta[2] + r;
-  if (row >= p.Nq * p.G) return;
-  const int kvh = meta[1], parts = meta[3] - (int)blockIdx.x + 1, tid = threadIdx.x;
-  auto slot = [&](int k) { return 2 * ((int64_t)blockIdx.x + k) + (k == 0 ? meta[4] : 0); };
-  // weights of the parts (at most 160)
-  float2 ml = make_float2(-INFINITY, 0.f);
-  if (tid < parts) ml = p.stat[slot(tid) * ROWS + r];
-  float top = ml.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
+  const int d4 = lane % LG, sub = lane / LG;
+  auto store = [&](const int* meta, float4 o, float top, float L) {
+    const int row = meta[2] + r, i = row / p.G, h = meta[1] * p.G + row % p.G;
+    const float inv = top == -INFINITY ? 0.f : 1.f / L;
+    *reinterpret_cast<uint2*>(p.o + (((int64_t)meta[0] * p.Nq + i) * p.Hq + h) * D + 4 * d4) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (d4 == 0)
+      p.lse[((int64_t)meta[0] * p.Hq + h) * p.Nq + i] =
+          top == -INFINITY ? -INFINITY : fmaf(top, p.scale_log2, log2f(L)) * kLn2;
+  };
+  auto add = [&](float4& o, int slot, float w) {
+    if (w == 0.f) return;  // a part that saw nothing
+    const float4 v = *reinterpret_cast<const float4*>(p.part + ((int64_t)slot * ROWS + r) * D + 4 * d4);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  };
+  auto fold = [&](float4& o) {  // the sub-groups of a warp
+    if (PP == 2) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+    }
+  };
+  auto parts_of = [&](int v) {
+    if (v >= workers) return 0;
+    const int* meta = p.meta + v * kMetaInts;
+    return meta[0] < 0 || meta[2] + r >= p.Nq * p.G ? 0 : meta[3] - v + 1;
+  };
+  const int v0 = blockIdx.x * 8;
+  {
+    const int v = v0 + warp, parts = parts_of(v);
+    if (parts > 0 && parts <= 32) {
+      const int* meta = p.meta + v * kMetaInts;
+      const int slot = 2 * (v + lane) + (lane == 0 ? meta[4] : 0);
+      const float2 ml = lane < parts ? p.stat[slot * ROWS + r] : make_float2(-INFINITY, 0.f);
+      float top = ml.x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((tid & 31) == 0) red[tid >> 5] = top;
-  __syncthreads();
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float w = ml.x == -INFINITY ? 0.f : fast_exp2((ml.x - top) * p.scale_log2);
+      float L = ml.y * w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, red[i]);
-  const float f = ml.x == -INFINITY ? 0.f : fast_exp2((ml.x - top) * p.scale_log2);
-  w[tid] = f;
-  float L = ml.y * f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  __syncthreads();
-  if ((tid & 31) == 0) red[tid >> 5] = L;
-  __syncthreads();
-  L = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) L += red[i];
-  const int grp = tid / LG, d4 = tid % LG;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = grp; k < parts; k += NGR) {
-    const float4 v = *reinterpret_cast<const float4*>(p.part + (slot(k) * ROWS + r) * D + 4 * d4);
-    const float wk = w[k];
-    if (wk == 0.f) continue;  // a part that saw nothing
-    o.x = fmaf(wk, v.x, o.x);
-    o.y = fmaf(wk, v.y, o.y);
-    o.z = fmaf(wk, v.z, o.z);
-    o.w = fmaf(wk, v.w, o.w);
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < parts; k += PP) {
+        const int kk = k + sub;
+        const float wk = __shfl_sync(0xffffffffu, w, kk & 31);
+        const int sl = __shfl_sync(0xffffffffu, slot, kk & 31);
+        if (kk < parts) add(o, sl, wk);
+      }
+      fold(o);
+      if (sub == 0) store(meta, o, top, L);
+    }
   }
-  buf[grp][d4] = o;
-  __syncthreads();
-  if (grp != 0) return;
+  for (int x = 0; x < 8; ++x) {
+    const int v = v0 + x, parts = parts_of(v);
+    if (parts <= 32) continue;
+    const int* meta = p.meta + v * kMetaInts;
+    auto slot_of = [&](int k) { return 2 * (v + k) + (k == 0 ? meta[4] : 0); };
+    float top = -INFINITY;
+    for (int k = tid; k < parts; k += 256) top = fmaxf(top, p.stat[slot_of(k) * ROWS + r].x);
 #pragma unroll
-  for (int k = 1; k < NGR; ++k) {
-    const float4 v = buf[k][d4];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    __syncthreads();
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, red[i]);
+    float L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < parts; k0 += 256) {
+      __syncthreads();
+      float w = 0.f;
+      if (k0 + tid < parts) {
+        const float2 ml = p.stat[slot_of(k0 + tid) * ROWS + r];
+        w = ml.x == -INFINITY ? 0.f : fast_exp2((ml.x - top) * p.scale_log2);
+        L = fmaf(ml.y, w, L);
+      }
+      wts[tid] = w;
+      __syncthreads();
+      const int m = min(256, parts - k0);
+#pragma unroll 4
+      for (int k = warp * PP + sub; k < m; k += 8 * PP) add(o, slot_of(k0 + k), wts[k]);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+    fold(o);
+    __syncthreads();
+    if (lane == 0) red[warp] = L;
+    buf[warp][lane] = o;
+    __syncthreads();
+    if (warp == 0) {
+      L = 0.f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        L += red[i];
+        const float4 b = buf[i][lane];
+        o.x += b.x;
+        o.y += b.y;
+        o.z += b.z;
+        o.w += b.w;
+      }
+      if (sub == 0) store(meta, o, top, L);
+    }
   }
-  const int i = row / p.G, h = kvh * p.G + row % p.G;
-  const float inv = top == -INFINITY ? 0.f : 1.f / L;
-  *reinterpret_cast<uint2*>(p.o + (((int64_t)b * p.Nq + i) * p.Hq + h) * D + 4 * d4) =
-      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (d4 == 0)
-    p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] =
-        top == -INFINITY ? -INFINITY : fmaf(top, p.scale_log2, log2f(L)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------
@@ -1087,11 +1201,11 @@ __global__ void __launch_bounds__(1024) paged_list_kernel(const __grid_constant_
 
 }  // namespace
 
-template <int D, int BITS, int NT>
+template <int D, int BITS, int NT, bool COOP>
 static cudaError_t launch_variant(const PagedAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                                   cudaStream_t st) {
   using C = Cfg<D, BITS, NT>;
-  auto* k = paged_attention_kernel<D, BITS, NT>;
+  auto* k = paged_attention_kernel<D, BITS, NT, COOP>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(k), C::kSmem);
   if (e != cudaSuccess) return e;
   if (p.list) {
@@ -1101,8 +1215,21 @@ static cudaError_t launch_variant(const PagedAttnParams& p, const CUtensorMap& t
     k<<<grid, C::kThreads, C::kSmem, st>>>(tk, tv, p);
     e = cudaGetLastError();
   }
-  if (e != cudaSuccess || p.uncut) return e;
-  return launch_after(paged_merge_kernel<D, C::kRows>, dim3(grid, C::kRows), dim3(256), 0, st, p);
+  if (e != cudaSuccess || p.mode != kPagedSplit) return e;
+  const int workers = grid * C::kWarps;
+  return launch_after(paged_merge_kernel<D, C::kRows>, dim3((workers + 7) / 8, std::min(C::kRows, p.Nq * p.G)), dim3(256),
+                      0, st, p, workers);
+}
+
+template <int D, int BITS>
+static cudaError_t launch_rows(const PagedAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                               cudaStream_t st) {
+  const bool coop = p.mode == kPagedCoop;
+  if (p.rows == 8)
+    return coop ? launch_variant<D, BITS, 1, true>(p, tk, tv, grid, st) : launch_variant<D, BITS, 1, false>(p, tk, tv, grid, st);
+  if (p.rows == 16)
+    return coop ? launch_variant<D, BITS, 2, true>(p, tk, tv, grid, st) : launch_variant<D, BITS, 2, false>(p, tk, tv, grid, st);
+  return coop ? launch_variant<D, BITS, 4, true>(p, tk, tv, grid, st) : launch_variant<D, BITS, 4, false>(p, tk, tv, grid, st);
 }
 
 int paged_tile_keys(int d, int bits) { return bits == 16 && d == 128 ? 32 : 64; }
@@ -1122,18 +1249,8 @@ cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& 
     const cudaError_t e = launch_after(paged_list_kernel, dim3(p.n_groups), dim3(1024), 0, st, p, plan);
     if (e != cudaSuccess) return e;
   }
-#define FM_PAGED(D, BITS)                                                              \
-  if (p.pg.d == D && p.pg.bits == BITS) {                                              \
-    if (p.rows == 8) return launch_variant<D, BITS, 1>(p, tk, tv, grid, st);           \
-    if (p.rows == 16) return launch_variant<D, BITS, 2>(p, tk, tv, grid, st);          \
-    return launch_variant<D, BITS, 4>(p, tk, tv, grid, st);                            \
-  }
-  FM_PAGED(64, 16)
-  FM_PAGED(128, 16)
-  FM_PAGED(64, 4)
-  FM_PAGED(128, 4)
-#undef FM_PAGED
-  return cudaErrorInvalidValue;
+  if (p.pg.d == 128) return p.pg.bits == 16 ? launch_rows<128, 16>(p, tk, tv, grid, st) : launch_rows<128, 4>(p, tk, tv, grid, st);
+  return p.pg.bits == 16 ? launch_rows<64, 16>(p, tk, tv, grid, st) : launch_rows<64, 4>(p, tk, tv, grid, st);
 }
 
 }  // namespace fm

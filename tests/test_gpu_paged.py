@@ -221,6 +221,22 @@ def test_attention_many_sequences(bits):
 
 
 @pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("Hm,cap", [(0, 0), (1, 0), (4, 3)])
+def test_attention_many_short_sequences(bits, Hm, cap):
+    """More items than a device takes at once, each of a few tiles: whole items per warp."""
+    rng = np.random.default_rng(4)
+    lens = [int(x) for x in rng.integers(0, 250, 150)]
+    lens[3], lens[149] = 256, 0
+    cache = Cache(25, lens, 2, 128, 32, bits).cuda()
+    vec = (None,) * 4 if Hm == 0 else masks("random", 150, Hm, 256, 5, 2)
+    fm.set_max_ctas(cap)
+    try:
+        check_attention(case_q(150, 2, 4, 128), cache, lens, vec)
+    finally:
+        fm.set_max_ctas(0)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
 def test_attention_long(bits):
     """One long sequence split over the whole device; every page also checked through its weights: keys are equal,
     so O is the mean of the values."""
@@ -246,9 +262,9 @@ def test_attention_long(bits):
 ])
 def test_attention_few_ctas_walk_many_items(bits, cap, kind, Nq, G, d, page):
     """Runs that hold many items and go round the ring of tiles several times."""
-    lens = [900, 0, 33, 1300, 64, 257]
+    lens = [900, 0, 33, 4100, 64, 257]
     cache, q = Cache(23, lens, 2, d, page, bits).cuda(), case_q(6, Nq, 2 * G, d)
-    vec = (None,) * 4 if kind == "none" else masks(kind, 6, 1, 1300, 8, Nq)
+    vec = (None,) * 4 if kind == "none" else masks(kind, 6, 1, 4100, 8, Nq)
     fm.set_max_ctas(cap)
     try:
         check_attention(q, cache, lens, vec)
