@@ -78,13 +78,10 @@ struct PagedAttnParams {
   uint64_t wait_limit_ns;
 };
 
-// What the plan kernels write: counts, list and words as above, and the class of every tile
-// (0 no pair visible, 1 some pair hidden, 2 all visible), [n_groups, list_stride].
+// What the plan kernel writes: counts, list and words as above.
 struct PlanOut {
   int *counts, *list;
   uint32_t* words;
-  uint8_t* flags;
-  int chunks;  // plan CTAs per group
 };
 
 constexpr int kPagedMaxCtas = 160;
@@ -117,6 +114,6 @@ cudaError_t launch_paged_gather(const GatherParams& p, cudaStream_t st);
 int paged_tile_keys(int d, int bits);
 // Plan (when p.list is set), attention and merge.
 cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                                   PlanOut plan, cudaStream_t st);
+                                   const PlanOut& plan, cudaStream_t st);
 
 }  // namespace fm

@@ -81,7 +81,7 @@ int check_paged_rows(const flashmask_pages* pg, const flashmask_paged_rows* r) {
 struct PagedLayout {
   int per_head, n_groups, mult, n_rb, rows, tile_keys, n_words, mode;
   int64_t keys;  // capacity of the table, in whole tiles
-  size_t part, stat, meta, counts, list, words, flags, bytes;
+  size_t part, stat, meta, counts, list, words, bytes;
 };
 
 PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& r) {
@@ -115,7 +115,6 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
     L.counts = take((size_t)L.n_groups * 4);
     L.list = take((size_t)L.n_groups * (L.keys / L.tile_keys) * 4);
     L.words = take((size_t)pg.B * r.Hm * L.n_words * L.keys * 4);
-    L.flags = take((size_t)L.n_groups * (L.keys / L.tile_keys));
   }
   L.bytes = off > 0 ? off : 256;
   return L;
@@ -247,7 +246,6 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
     p.counts = plan.counts = reinterpret_cast<int*>(ws + L.counts);
     p.list = plan.list = reinterpret_cast<int*>(ws + L.list);
     p.words = plan.words = reinterpret_cast<uint32_t*>(ws + L.words);
-    plan.flags = ws + L.flags;
     p.list_stride = (int)(L.keys / L.tile_keys);
     p.n_words = L.n_words;
     p.words_stride = L.keys;

@@ -14,8 +14,8 @@
 //    equal calls give equal bits).  Lengths are device data and the grid does
 //    not depend on them, so a captured graph serves growing sequences.
 //  - Warps work alone: each looks its pages up, fills a ring of tiles of its
-//    own in shared memory by TMA (swizzled boxes for bf16, plain bulk copies
-//    for 4 bits) and keeps its own running maximum and sums; the ring runs on
+//    own in shared memory (bf16: TMA, swizzled boxes; 4 bits: cp.async, whole
+//    code rows) and keeps its own running maximum and sums; the ring runs on
 //    into the next item, so the loads never pause at an item's end.
 //  - Few short items (a table of a few tiles per warp) take one CTA each
 //    instead, whose warps share the tiles and join their sums in shared memory.
@@ -26,12 +26,14 @@
 //    K Q^T and O^T = V^T P^T need only 8 row columns, where the usual
 //    orientation pads the rows to 16.  mma.sync and not tcgen05: rows are
 //    few, P never leaves registers, and the tensor pipe is far from the bound.
-//  - 4 bits.  A row's codes enter the products as the integers code - 8 (exact
-//    in bf16); scale and minimum are applied to sums in fp32:
+//  - 4 bits.  A row's codes enter the products as integers, exact in bf16 (K:
+//    16 + code, which costs no subtraction, with -24 sum(q) as the sum's first
+//    value; V: code - 8); scale and minimum are applied to sums in fp32:
 //      q.k = s (q.(c - 8)) + (m + 8 s) sum(q)
 //      o   = sum (p s)(c - 8) + sum p (m + 8 s)
 //    The contraction may run over the head's values in any order as long as
 //    both sides agree, so each thread takes whole 16-byte pieces of code rows.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -39,6 +41,8 @@
 #include "launchers.h"
 #include "paged.cuh"
 #include "sm100_primitives.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace fm {
 namespace {
@@ -51,22 +55,34 @@ constexpr int kMetaInts = 8;
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int group_batch(const PagedAttnParams& p, int g) { return p.per_head ? g / p.pg.Hkv : g; }
 
-// Keys of sequence b that its rows can see at all, and its first row's position.
-__device__ __forceinline__ int key_bound(const PagedAttnParams& p, int b, int* len_out, int64_t* first) {
-  const int len = checked_len(p.pg, p.lens, b);
-  const int64_t st = p.start ? (int64_t)p.start[b] : (int64_t)len - p.Nq;
-  *len_out = len;
-  *first = st;
-  const int64_t hi = p.causal ? min((int64_t)len, st + p.Nq) : (int64_t)len;
+// A sequence as the kernels use it: cached keys, and its first row's position.
+struct Seq {
+  int len, first;
+};
+__device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
+  Seq q;
+  q.len = checked_len(p.pg, p.lens, b);
+  q.first = p.start ? p.start[b] : q.len - p.Nq;
+  return q;
+}
+// Keys that the sequence's rows can see at all.
+__device__ __forceinline__ int key_bound(const PagedAttnParams& p, const Seq& q) {
+  const int64_t hi = p.causal ? min((int64_t)q.len, (int64_t)q.first + p.Nq) : (int64_t)q.len;
   return hi > 0 ? (int)hi : 0;
 }
 
-__device__ __forceinline__ int tiles_of(const PagedAttnParams& p, int g) {
-  if (p.counts) return p.counts[g];
-  int len;
-  int64_t st;
-  return (key_bound(p, group_batch(p, g), &len, &st) + p.tile_keys - 1) / p.tile_keys;
-}
+// The CTA's copy of the sequences (and, with lists, of the groups' tile
+// counts): once the rings are filled a load from memory waits behind them.
+constexpr int kSeqCache = 512;
+struct Seqs {
+  const Seq* seq;     // shared memory, or null: too many to hold
+  const int* counts;
+  __device__ __forceinline__ Seq get(const PagedAttnParams& p, int b) const { return seq ? seq[b] : load_seq(p, b); }
+  __device__ __forceinline__ int tiles(const PagedAttnParams& p, int g) const {
+    if (p.counts) return counts ? counts[g] : p.counts[g];
+    return (key_bound(p, get(p, group_batch(p, g))) + p.tile_keys - 1) / p.tile_keys;
+  }
+};
 
 // A run, walked segment by segment (a segment: tiles [t, t + n) of one item).
 // Runs are made of units (tiles), or of whole items.
@@ -74,7 +90,7 @@ struct Walk {
   int g, in, t, T;  // group, item in the group, first tile, tiles of the group's items
   int left;         // units (items) left in the run
   int n;            // tiles of this segment
-  __device__ __forceinline__ bool next(const PagedAttnParams& p) {
+  __device__ __forceinline__ bool next(const PagedAttnParams& p, const Seqs& sq) {
     left -= p.mode == kPagedSplit ? n : 1;
     if (left <= 0) return false;
     t = 0;
@@ -82,7 +98,7 @@ struct Walk {
       in = 0;
       do {
         ++g;
-        T = tiles_of(p, g);
+        T = sq.tiles(p, g);
       } while (T == 0 && p.mode == kPagedSplit);
     }
     n = p.mode == kPagedSplit ? min(T, left) : T;
@@ -125,7 +141,7 @@ struct Cfg {
   static constexpr int kMerge = kWarps * kRows * kStride * 4;   // on top of the rings
   static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;  // per warp
   static constexpr int kPerStage = kStage + 16 + 8;             // + header, barrier
-  static constexpr int kFixed = kWarps * (kQBytes + 4 * kRows * 4) + 1024 + 256;
+  static constexpr int kFixed = kWarps * (kQBytes + 4 * kRows * 4) + kSeqCache * 12 + 1024 + 256;
   // Every warp has a ring of its own, which it fills and empties itself: a stage is refilled by the warp
   // that has just read it, so nothing waits for another warp.
   static constexpr int kFit = (225 * 1024 - kFixed) / kPerStage / kWarps;
@@ -146,6 +162,8 @@ struct Smem {
   uint2* q;            // Q fragments of each warp (kQShared)
   float *m, *l, *c;    // kWarps x kRows (one item per CTA)
   float* qsum;         // kWarps x kRows
+  Seq* seq;            // kSeqCache
+  int* counts;         // kSeqCache
   int* abort;
   __device__ __forceinline__ explicit Smem(uint8_t* raw) {
     const uint32_t a = smem_addr(raw);
@@ -158,6 +176,8 @@ struct Smem {
     l = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
     c = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
     qsum = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
+    seq = reinterpret_cast<Seq*>(x); x += kSeqCache * 8;
+    counts = reinterpret_cast<int*>(x); x += kSeqCache * 4;
     abort = reinterpret_cast<int*>(x);
   }
 };
@@ -193,7 +213,24 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map,
       : "memory");
 }
 
-// Codes at nibbles i and i + 4 of each half of x as the bf16 pair (code - 8):
+// 16 bytes per lane, global to shared memory; a group of them is one tile.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
+
+// The code at nibble i of each half of x as the bf16 pair 16 + code: the four
+// bits become the upper mantissa bits of 16.0.
+__device__ __forceinline__ uint32_t raised(uint32_t x, int i) {
+  uint32_t y;
+  const uint32_t v = i == 0 ? x << 3 : x >> (4 * i - 3);
+  asm("lop3.b32 %0, %1, 0x00780078, 0x41804180, 0xea;" : "=r"(y) : "r"(v));  // (v & a) | b
+  return y;
+}
+
+// The code at nibble i of each half of x as the bf16 pair code - 8:
 // 0x4300 + code is 128 + code, and 128 + code - 136 is exact.
 __device__ __forceinline__ uint32_t centred(uint32_t x, int i) {
   uint32_t y;
@@ -234,14 +271,13 @@ struct Issuer {
   int kvh;
   int j0, flags, page[C::kBoxes];  // a lane's tile: first key, masked | valid boxes << 1, pages
 
-  __device__ __forceinline__ void batch(const PagedAttnParams& p, int box_shift) {
+  __device__ __forceinline__ void batch(const PagedAttnParams& p, const Seqs& sq, int box_shift) {
     constexpr int KT = C::kKT;
     const int lane = threadIdx.x & 31, boxes = KT >> box_shift;
     const Item it = item_of(p, w.g, w.in, C::kRows);
     kvh = it.kvh;
-    int len;
-    int64_t first;
-    const int hi = key_bound(p, it.b, &len, &first);
+    const Seq seq = sq.get(p, it.b);
+    const int hi = key_bound(p, seq);
     nb = min(32, (w.n - k + STEP - 1) / STEP);
     x = 0;
     j0 = 0;
@@ -257,7 +293,7 @@ struct Issuer {
       } else {
         j0 = t * KT;
         // keys that every row of the item sees
-        const int64_t all = p.causal ? min((int64_t)len, first + it.row0 / p.G + 1) : (int64_t)len;
+        const int64_t all = p.causal ? min((int64_t)seq.len, (int64_t)seq.first + it.row0 / p.G + 1) : (int64_t)seq.len;
         masked = (int64_t)j0 + KT > all;
       }
 #pragma unroll
@@ -283,18 +319,18 @@ struct Issuer {
   }
 
   __device__ __forceinline__ void issue(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
-                                        const Smem<D, BITS, NT>& sm, int warp, int box_shift) {
+                                        const Smem<D, BITS, NT>& sm, const Seqs& sq, int warp, int box_shift) {
     if (x == nb) {
       if (!more) return;
       while (k >= w.n) {
         k -= w.n;
-        if (!w.next(p)) {
+        if (!w.next(p, sq)) {
           more = false;
           x = nb = 0;
           return;
         }
       }
-      batch(p, box_shift);
+      batch(p, sq, box_shift);
     }
     const int lane = threadIdx.x & 31;
     const int tj = __shfl_sync(0xffffffffu, j0, x), f = __shfl_sync(0xffffffffu, flags, x);
@@ -303,27 +339,35 @@ struct Issuer {
     uint8_t* st = sm.stage + stage * C::kStage;
     if (lane == 0) {
       sm.hdr[stage] = make_int4(tj, f & 1, f >> 1, 0);
-      mbar_arrive_expect_tx(bar, (uint32_t)(__popc(f >> 1) << box_shift) * (2 * C::kRowBytes + (BITS == 4 ? 8 : 0)));
+      if (BITS == 16)
+        mbar_arrive_expect_tx(bar, (uint32_t)(__popc(f >> 1) << box_shift) * (2 * C::kRowBytes));
     }
 #pragma unroll
     for (int i = 0; i < C::kBoxes; ++i) {
       if (i >= (C::kKT >> box_shift)) break;
       const int pid = __shfl_sync(0xffffffffu, page[i], x);
-      if (lane == 0 && ((f >> (1 + i)) & 1)) {
-        const int64_t row = row_of(p.pg, pid, kvh, tj + (i << box_shift));
-        if (BITS == 16) {
+      if (!((f >> (1 + i)) & 1)) continue;
+      const int64_t row = row_of(p.pg, pid, kvh, tj + (i << box_shift));
+      if (BITS == 16) {
+        if (lane == 0) {
           uint8_t* dst = st + (i << box_shift) * C::kRowBytes;
           tma_load_rows(dst, tk, bar, (int)row);
           tma_load_rows(dst + C::kHalf, tv, bar, (int)row);
-        } else {
-          const uint32_t bytes = (uint32_t)C::kRowBytes << box_shift;
-          uint8_t* dst = st + (i << box_shift) * C::kRowBytes;
-          bulk_load(dst, p.pg.k + row * C::kRowBytes, bytes, bar);
-          bulk_load(dst + C::kHalf, p.pg.v + row * C::kRowBytes, bytes, bar);
-          uint8_t* sc = st + 2 * C::kHalf + (i << box_shift) * 4;
-          bulk_load(sc, p.pg.k_scales + row, 4u << box_shift, bar);
-          bulk_load(sc + C::kScales, p.pg.v_scales + row, 4u << box_shift, bar);
         }
+      } else {
+        // Every lane copies 16-byte pieces: four bulk copies a tile kept the copy engine, which takes some
+        // 60 ns for each whatever its size, busier than the memory.
+        const uint32_t dst = smem_addr(st) + (i << box_shift) * C::kRowBytes + lane * 16;
+        const uint8_t* sk = p.pg.k + row * C::kRowBytes + lane * 16;
+        const uint8_t* sv = p.pg.v + row * C::kRowBytes + lane * 16;
+#pragma unroll 2
+        for (int c = 0; c < (C::kRowBytes << box_shift); c += 512) {
+          copy16(dst + c, sk + c);
+          copy16(dst + C::kHalf + c, sv + c);
+        }
+        if ((lane & 15) < (1 << box_shift) / 4)  // scales and minima: K by the lower half of the warp, V by the upper
+          copy16(smem_addr(st) + 2 * C::kHalf + (lane >> 4) * C::kScales + (i << box_shift) * 4 + (lane & 15) * 16,
+                 (lane < 16 ? p.pg.k_scales : p.pg.v_scales) + row + (lane & 15) * 4);
       }
     }
     ++x;
@@ -336,7 +380,8 @@ struct Issuer {
 // each segment.
 template <int D, int BITS, int NT, bool COOP>
 __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
-                                       const Smem<D, BITS, NT>& sm, Walk wk, const WaitCtx& wc, const Run& run) {
+                                       const Smem<D, BITS, NT>& sm, const Seqs& sq, Walk wk, const WaitCtx& wc,
+                                       const Run& run) {
   using C = Cfg<D, BITS, NT>;
   constexpr int KT = C::kKT, MT = D / 16, KS = D / 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -344,70 +389,52 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
   const int box_shift = min(p.pg.page_shift, KT == 32 ? 5 : 6);
   const uint32_t box_rows = 1u << box_shift;
   constexpr int STEP = COOP ? C::kWarps : 1;
-  Issuer<D, BITS, NT, STEP> is;
-  is.start(wk, COOP ? warp : 0);
-#pragma unroll 1
-  for (int i = 0; i < C::kDepth; ++i) is.issue(p, tk, tv, sm, warp, box_shift);
-  int k = COOP ? warp : 0, taken = 0;  // the warp's next tile in the segment, and the tiles it has taken
-  bool alive = true, first_seg = true;
-  int u = run.u0;  // first unit of the segment
-  do {
-    const Item it = item_of(p, wk.g, wk.in, C::kRows);
-    int len;
-    int64_t first;
-    key_bound(p, it.b, &len, &first);
-    const int R = p.Nq * p.G - it.row0;  // real rows of the block (may exceed kRows)
-    const __nv_bfloat16* qb = p.q + it.b * p.qs[0];
 
-    // ---- Q fragments (B operand of S^T: k = values of the head, n = rows) ----
-    uint2 qf[C::kQShared ? 1 : KS][C::kQShared ? 1 : NT];
-    float qsum[2 * NT];
-    auto load_q = [&](int ks, int nt) {
+  // ---- Q fragments (B operand of S^T: k = values of the head, n = rows) ----
+  // A lane's pieces of its row of each 8: for 4 bits values base + {0, 1} and base + {4, 5}, which
+  // turn_q() pairs as centred() pairs the codes.
+  uint2 qf[C::kQShared ? 1 : KS][C::kQShared ? 1 : NT];
+  float qsum[2 * NT];
+  uint2* qw = sm.q + warp * (C::kQBytes / 8);
+  auto row_ptr = [&](const Item& it, int r) {
+    const int row = it.row0 + r, i = row / p.G;
+    return p.q + it.b * p.qs[0] + i * p.qs[1] + (it.kvh * p.G + row - i * p.G) * p.qs[2];
+  };
+  auto load_q = [&](const Item& it) {
+    const int R = p.Nq * p.G - it.row0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g8;
-      if (r >= R) return make_uint2(0u, 0u);
-      const int row = it.row0 + r, i = row / p.G, h = it.kvh * p.G + row % p.G;
-      const __nv_bfloat16* src = qb + i * p.qs[1] + h * p.qs[2];
-      if (BITS == 16) {
-        const uint32_t* s = reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * q4);
-        return make_uint2(s[0], s[4]);
-      } else {
-        // values base + {0, 4} and base + {1, 5}: the nibble pairs that centred() gives
-        const uint32_t* s = reinterpret_cast<const uint32_t*>(src + (D / 4) * q4 + 8 * (ks >> 1) + 2 * (ks & 1));
-        const uint32_t lo = s[0], hi = s[2];
-        return make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
-      }
-    };
-    if (!C::kQShared) {
+      const __nv_bfloat16* src = row_ptr(it, min(r, R - 1));
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt] = load_q(ks, nt);
-      if (BITS == 4) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float s = 0.f;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const uint2 u = qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
-            s += (__uint_as_float(u.x << 16) + __uint_as_float(u.x & 0xffff0000u)) +
-                 (__uint_as_float(u.y << 16) + __uint_as_float(u.y & 0xffff0000u));
-          }
-          s += __shfl_xor_sync(0xffffffffu, s, 1);
-          s += __shfl_xor_sync(0xffffffffu, s, 2);  // lanes of row g8 hold its sum
-          qsum[2 * nt] = __shfl_sync(0xffffffffu, s, 8 * q4);
-          qsum[2 * nt + 1] = __shfl_sync(0xffffffffu, s, 8 * q4 + 4);
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint32_t* a = reinterpret_cast<const uint32_t*>(
+            BITS == 16 ? src + ks * 16 + 2 * q4 : src + (D / 4) * q4 + 8 * (ks >> 1) + 2 * (ks & 1));
+        uint2 v = make_uint2(a[0], a[BITS == 16 ? 4 : 2]);
+        if (C::kQShared) {
+          if (r >= R) v = make_uint2(0u, 0u);
+          qw[(ks * NT + nt) * 32 + lane] =
+              BITS == 16 ? v : make_uint2(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632));
+        } else {
+          qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt] = v;
         }
       }
-    } else {
-      uint2* qw = sm.q + warp * (C::kQBytes / 8);
-#pragma unroll 4
-      for (int x = 0; x < KS * NT; ++x) qw[x * 32 + lane] = load_q(x / NT, x % NT);
+    }
+  };
+  auto turn_q = [&](const Item& it) {
+    const int R = p.Nq * p.G - it.row0;
+    if (C::kQShared) {
       if (BITS == 4) {
         float s = 0.f;
         if (lane < C::kRows && lane < R) {
-          const int row = it.row0 + lane, i = row / p.G, h = it.kvh * p.G + row % p.G;
-          const __nv_bfloat16* src = qb + i * p.qs[1] + h * p.qs[2];
-          for (int x = 0; x < D; ++x) s += __bfloat162float(src[x]);
+          const uint4* src = reinterpret_cast<const uint4*>(row_ptr(it, lane));
+#pragma unroll 2
+          for (int x = 0; x < D / 8; ++x) {
+            const uint4 u = src[x];
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) s += __uint_as_float(w[y] << 16) + __uint_as_float(w[y] & 0xffff0000u);
+          }
         }
         if (lane < C::kRows) sm.qsum[warp * C::kRows + lane] = s;
       }
@@ -419,8 +446,50 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
           qsum[2 * nt + 1] = sm.qsum[warp * C::kRows + nt * 8 + 2 * q4 + 1];
         }
       }
+      return;
     }
-    const uint2* qw = sm.q + warp * (C::kQBytes / 8);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float s = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint2& u = qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
+        if (nt * 8 + g8 >= R) u = make_uint2(0u, 0u);
+        if (BITS == 4) {
+          u = make_uint2(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.x, u.y, 0x7632));
+          s += (__uint_as_float(u.x << 16) + __uint_as_float(u.x & 0xffff0000u)) +
+               (__uint_as_float(u.y << 16) + __uint_as_float(u.y & 0xffff0000u));
+        }
+      }
+      if (BITS == 4) {
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);  // lanes of row g8 hold its sum
+        qsum[2 * nt] = __shfl_sync(0xffffffffu, s, 8 * q4);
+        qsum[2 * nt + 1] = __shfl_sync(0xffffffffu, s, 8 * q4 + 4);
+      }
+    }
+  };
+
+  Item it = item_of(p, wk.g, wk.in, C::kRows);
+  load_q(it);  // before the rings: what is loaded after them waits behind them
+  Issuer<D, BITS, NT, STEP> is;
+  is.start(wk, COOP ? warp : 0);
+#pragma unroll 1
+  for (int i = 0; i < C::kDepth; ++i) {
+    is.issue(p, tk, tv, sm, sq, warp, box_shift);
+    if (BITS == 4) copy_commit();
+  }
+  int k = COOP ? warp : 0, taken = 0;  // the warp's next tile in the segment, and the tiles it has taken
+  bool alive = true, first_seg = true;
+  int u = run.u0;  // first unit of the segment
+  do {
+    if (!first_seg) {
+      it = item_of(p, wk.g, wk.in, C::kRows);
+      load_q(it);
+    }
+    const Seq seq = sq.get(p, it.b);
+    const int R = p.Nq * p.G - it.row0;  // real rows of the block (may exceed kRows)
+    turn_q(it);
 
     float acc[MT][NT][4], mx[2 * NT], sum[2 * NT], cor[2 * NT];
 #pragma unroll
@@ -438,9 +507,14 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
 
     for (; k < wk.n; k += STEP) {
       const int stage = warp * C::kDepth + taken % C::kDepth;
-      if (alive) alive = mbar_wait(&sm.full[stage], (taken / C::kDepth) & 1u, wc);
-      alive = __all_sync(0xffffffffu, alive);
-      if (!alive) continue;
+      if (BITS == 16) {
+        if (alive) alive = mbar_wait(&sm.full[stage], (taken / C::kDepth) & 1u, wc);
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) continue;
+      } else {
+        copy_wait<C::kDepth - 1>();
+        __syncwarp();
+      }
       ++taken;
       const int4 hd = sm.hdr[stage];
       uint8_t* st = sm.stage + stage * C::kStage;
@@ -462,7 +536,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[m2][nt][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[m2][nt][e] = BITS == 4 ? -24.f * qsum[2 * nt + (e & 1)] : 0.f;  // 16 + code -> code - 8
         if (BITS == 16) {
           const uint32_t lrow = ((lane & 7) + ((lane >> 3) & 1) * 8) * 128, hi = lane >> 4;
 #pragma unroll
@@ -495,8 +569,8 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
               const int i = 2 * (ks & 1);
-              const uint32_t a[4] = {centred(r0[ks >> 1], i), centred(r1[ks >> 1], i), centred(r0[ks >> 1], i + 1),
-                                     centred(r1[ks >> 1], i + 1)};
+              const uint32_t a[4] = {raised(r0[ks >> 1], i), raised(r1[ks >> 1], i), raised(r0[ks >> 1], i + 1),
+                                     raised(r1[ks >> 1], i + 1)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 const uint2 b = C::kQShared ? qw[(ks * NT + nt) * 32 + lane] : qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
@@ -554,7 +628,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
                       see = (p.words[at] >> (i & 31)) & 1u;
                     }
                   } else {
-                    see = j < len && (!p.causal || j <= first + i);
+                    see = j < seq.len && (!p.causal || j <= (int64_t)seq.first + i);
                   }
                   if (!(see && there)) {
                     hid |= 1u << ((m2 * 2 + hf) * 2 * NT + nt * 2 + e);
@@ -711,9 +785,10 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
           }
         }
       }
-      if (wrote) fence_async_smem();
+      if (BITS == 16 && wrote) fence_async_smem();
       __syncwarp();
-      is.issue(p, tk, tv, sm, warp, box_shift);
+      is.issue(p, tk, tv, sm, sq, warp, box_shift);
+      if (BITS == 4) copy_commit();  // a group per tile, empty at the run's end
     }
     k -= wk.n;
 
@@ -859,8 +934,8 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
     }
     first_seg = false;
     u += wk.n;
-  } while (wk.next(p));
-  if (!alive && lane == 0) {  // gave up: let the copies in flight land before the CTA ends
+  } while (wk.next(p, sq));
+  if (BITS == 16 && !alive && lane == 0) {  // gave up: let the copies in flight land before the CTA ends
     WaitCtx w2 = wc;
     int zero = 0;
     w2.abort = &zero;
@@ -899,18 +974,27 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
   wc.limit_ns = p.wait_limit_ns;
   wc.smem_base = smem_addr(raw);
   wc.kernel = 5;
-  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
+  Seqs sq{nullptr, nullptr};
+  if (p.pg.B <= kSeqCache) {
+    for (int b = tid; b < p.pg.B; b += C::kThreads) sm.seq[b] = load_seq(p, b);
+    sq.seq = sm.seq;
+  }
+  if (p.counts && p.n_groups <= kSeqCache) {
+    for (int g = tid; g < p.n_groups; g += C::kThreads) sm.counts[g] = p.counts[g];
+    sq.counts = sm.counts;
+  }
+  __syncthreads();
 
   Walk wk;
   if (COOP) {  // one item per CTA
     wk.g = blockIdx.x / p.mult;
     wk.in = blockIdx.x % p.mult;
     wk.t = 0;
-    wk.T = wk.n = tiles_of(p, wk.g);
+    wk.T = wk.n = sq.tiles(p, wk.g);
     wk.left = 1;
-    attend<D, BITS, NT, true>(p, &tk, &tv, sm, wk, wc, Run{});
+    attend<D, BITS, NT, true>(p, &tk, &tv, sm, sq, wk, wc, Run{});
     return;
   }
   // neighbouring runs go to different SMs: a small problem's few runs are spread over the device
@@ -923,8 +1007,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
     wk.g = first / p.mult;
     wk.in = first % p.mult;
     wk.t = 0;
-    wk.T = wk.n = tiles_of(p, wk.g);
-    attend<D, BITS, NT, false>(p, &tk, &tv, sm, wk, wc, Run{});
+    wk.T = wk.n = sq.tiles(p, wk.g);
+    attend<D, BITS, NT, false>(p, &tk, &tv, sm, sq, wk, wc, Run{});
     return;
   }
 
@@ -932,7 +1016,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
   const int per = (p.n_groups + 31) / 32, ga = min(lane * per, p.n_groups), gb = min(ga + per, p.n_groups);
   int mine = 0;
 #pragma unroll 4
-  for (int g = ga; g < gb; ++g) mine += tiles_of(p, g);
+  for (int g = ga; g < gb; ++g) mine += sq.tiles(p, g);
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -951,10 +1035,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
     wk.g = ga;
     wk.T = 0;
     if (lane == src) {
-      wk.T = tiles_of(p, wk.g);
+      wk.T = sq.tiles(p, wk.g);
       while (u0 >= at + wk.T * p.mult) {
         at += wk.T * p.mult;
-        wk.T = tiles_of(p, ++wk.g);
+        wk.T = sq.tiles(p, ++wk.g);
       }
     }
     wk.g = __shfl_sync(0xffffffffu, wk.g, src);
@@ -964,10 +1048,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
     wk.t = off - wk.in * wk.T;
     wk.left = n_units;
     wk.n = min(wk.T - wk.t, n_units);
-    attend<D, BITS, NT, false>(p, &tk, &tv, sm, wk, wc, Run{worker, u0, q, rem});
+    attend<D, BITS, NT, false>(p, &tk, &tv, sm, sq, wk, wc, Run{worker, u0, q, rem});
   }
   for (int g = blockIdx.x; g < p.n_groups; g += gridDim.x)
-    if (tiles_of(p, g) == 0) write_empty<D>(p, g, C::kThreads);
+    if (sq.tiles(p, g) == 0) write_empty<D>(p, g, C::kThreads);
 }
 
 // ---------------------------------------------------------------------------
@@ -978,6 +1062,7 @@ template <int D, int ROWS>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int workers) {
   constexpr int LG = D / 4, PP = 32 / LG;  // lanes of a row, parts that a warp reads at a time
   __shared__ float red[8], wts[256];
+  __shared__ int metas[8][kMetaInts];
   __shared__ float4 buf[8][32];
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
@@ -1007,16 +1092,17 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
       o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
     }
   };
-  auto parts_of = [&](int v) {
-    if (v >= workers) return 0;
-    const int* meta = p.meta + v * kMetaInts;
-    return meta[0] < 0 || meta[2] + r >= p.Nq * p.G ? 0 : meta[3] - v + 1;
-  };
   const int v0 = blockIdx.x * 8;
+  if (tid < 8 * kMetaInts) {
+    const int v = v0 + tid / kMetaInts;
+    metas[tid / kMetaInts][tid % kMetaInts] = v < workers ? p.meta[v0 * kMetaInts + tid] : -1;
+  }
+  __syncthreads();
+  auto parts_of = [&](int x) { return metas[x][0] < 0 || metas[x][2] + r >= p.Nq * p.G ? 0 : metas[x][3] - (v0 + x) + 1; };
   {
-    const int v = v0 + warp, parts = parts_of(v);
+    const int v = v0 + warp, parts = parts_of(warp);
     if (parts > 0 && parts <= 32) {
-      const int* meta = p.meta + v * kMetaInts;
+      const int* meta = metas[warp];
       const int slot = 2 * (v + lane) + (lane == 0 ? meta[4] : 0);
       const float2 ml = lane < parts ? p.stat[slot * ROWS + r] : make_float2(-INFINITY, 0.f);
       float top = ml.x;
@@ -1039,9 +1125,9 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
     }
   }
   for (int x = 0; x < 8; ++x) {
-    const int v = v0 + x, parts = parts_of(v);
+    const int v = v0 + x, parts = parts_of(x);
     if (parts <= 32) continue;
-    const int* meta = p.meta + v * kMetaInts;
+    const int* meta = metas[x];
     auto slot_of = [&](int k) { return 2 * (v + k) + (k == 0 ? meta[4] : 0); };
     float top = -INFINITY;
     for (int k = tid; k < parts; k += 256) top = fmaxf(top, p.stat[slot_of(k) * ROWS + r].x);
@@ -1093,10 +1179,13 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
 }
 
 // ---------------------------------------------------------------------------
-// plan: row-visibility words and tile flags (one warp per tile), then the list
-// of visible tiles (one CTA per group)
+// plan: row-visibility words and the list of visible tiles.  One cluster of 8
+// CTAs per group: each CTA reads an eighth of the group's mask vectors, one
+// warp per tile, and the CTAs exchange their counts through distributed shared
+// memory, so that one launch both reads the vectors with 256 warps and leaves
+// the list in order.
 // ---------------------------------------------------------------------------
-constexpr int kPlanTiles = 64;  // tiles of one CTA (8 warps)
+constexpr int kPlanCtas = 8, kPlanThreads = 1024, kPlanTiles = 4096;  // tiles of one CTA at a time
 
 // Rows [p0, p0 + 32) with [lo, hi) cut out, as a word.
 __device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t p0) {
@@ -1105,77 +1194,83 @@ __device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t p0) 
 }
 
 template <int KT>
-__global__ void __launch_bounds__(256) paged_plan_kernel(const __grid_constant__ PagedAttnParams p, PlanOut out) {
-  griddep_wait();
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    paged_plan_kernel(const __grid_constant__ PagedAttnParams p, PlanOut out) {
+  __shared__ uint8_t flag[kPlanTiles];
+  __shared__ int cnt, wsum[32];
   griddep_launch_dependents();
-  const int g = blockIdx.x / out.chunks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank(), g = blockIdx.x / kPlanCtas;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = group_batch(p, g);
   const int hm0 = p.per_head ? (g % p.pg.Hkv) * p.G : 0, nh = p.per_head ? p.G : 1;
-  int len;
-  int64_t first;
-  const int hi = key_bound(p, b, &len, &first);
-  const int tiles = (hi + KT - 1) / KT;
+  const Seq seq = load_seq(p, b);
+  const int hi = key_bound(p, seq), tiles = (hi + KT - 1) / KT;
+  int done = 0;
+  for (int t0 = 0; t0 < tiles; t0 += kPlanCtas * kPlanTiles) {
+    const int block = min(tiles - t0, kPlanCtas * kPlanTiles), share = (block + kPlanCtas - 1) / kPlanCtas;
+    const int a = min(rank * share, block), n = min(share, block - a);  // this CTA's tiles: t0 + a + [0, n)
+    int seen = 0;
 #pragma unroll 2
-  for (int x = warp; x < kPlanTiles; x += 8) {
-    const int t = (blockIdx.x % out.chunks) * kPlanTiles + x;
-    if (t >= tiles) break;
-    bool any = false, all = true;
+    for (int t = warp; t < n; t += 32) {
+      bool any = false, all = true;
 #pragma unroll
-    for (int jj = 0; jj < KT; jj += 32) {
-      const int j = t * KT + jj + lane;
-      for (int h = 0; h < nh; ++h) {
-        const int64_t at = ((int64_t)b * p.Hm + hm0 + h);
-        int lts = 0, lte = 0, uts = 0, ute = 0;
-        if (j < p.Nm && j < hi) {
-          const int64_t m = at * p.Nm + j;
-          if (p.lts) {
-            lts = p.lts[m];
-            lte = p.lte[m];
+      for (int jj = 0; jj < KT; jj += 32) {
+        const int j = (t0 + a + t) * KT + jj + lane;
+        for (int h = 0; h < nh; ++h) {
+          const int64_t at = ((int64_t)b * p.Hm + hm0 + h);
+          int lts = 0, lte = 0, uts = 0, ute = 0;
+          if (j < p.Nm && j < hi) {
+            const int64_t m = at * p.Nm + j;
+            if (p.lts) {
+              lts = p.lts[m];
+              lte = p.lte[m];
+            }
+            if (p.uts) {
+              uts = p.uts[m];
+              ute = p.ute[m];
+            }
           }
-          if (p.uts) {
-            uts = p.uts[m];
-            ute = p.ute[m];
+          for (int w = 0; w < p.n_words; ++w) {
+            const int64_t p0 = (int64_t)seq.first + 32 * w;
+            const uint32_t rows = bit_range(0, min(32, p.Nq - 32 * w));
+            uint32_t see = 0;
+            if (j < hi) {
+              uint32_t hid = rows_in(lts, lte, p0) | rows_in(uts, ute, p0);
+              if (p.causal) hid |= rows_in(p0, j, p0);
+              see = rows & ~hid;
+            }
+            out.words[(at * p.n_words + w) * p.words_stride + j] = see;
+            any |= see != 0;
+            all &= see == rows;
           }
-        }
-        for (int w = 0; w < p.n_words; ++w) {
-          const int64_t p0 = first + 32 * w;
-          const uint32_t rows = bit_range(0, min(32, p.Nq - 32 * w));
-          uint32_t see = 0;
-          if (j < hi) {
-            uint32_t hid = rows_in(lts, lte, p0) | rows_in(uts, ute, p0);
-            if (p.causal) hid |= rows_in(p0, j, p0);
-            see = rows & ~hid;
-          }
-          out.words[(at * p.n_words + w) * p.words_stride + j] = see;
-          any |= see != 0;
-          all &= see == rows;
         }
       }
+      any = __any_sync(0xffffffffu, any);
+      all = __all_sync(0xffffffffu, all);
+      if (lane == 0) flag[t] = any ? (all ? 2 : 1) : 0;
+      seen += any;
     }
-    any = __any_sync(0xffffffffu, any);
-    all = __all_sync(0xffffffffu, all);
-    if (lane == 0) out.flags[(int64_t)g * p.list_stride + t] = any ? (all ? 2 : 1) : 0;
-  }
-}
-
-__global__ void __launch_bounds__(1024) paged_list_kernel(const __grid_constant__ PagedAttnParams p, PlanOut out) {
-  __shared__ int wsum[32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int len;
-  int64_t first;
-  const int hi = key_bound(p, group_batch(p, g), &len, &first);
-  const int tiles = (hi + p.tile_keys - 1) / p.tile_keys;
-  const uint8_t* flags = out.flags + (int64_t)g * p.list_stride;
-  int* list = out.list + (int64_t)g * p.list_stride;
-  int done = 0;
-  for (int t0 = 0; t0 < tiles; t0 += 4096) {  // four tiles a thread at a time
+    if (lane == 0) wsum[warp] = seen;
+    __syncthreads();
+    if (warp == 0) {
+      int v = wsum[lane];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) cnt = v;
+    }
+    cl.sync();
+    int at = done, total = 0;
+    for (int r = 0; r < kPlanCtas; ++r) {
+      const int c = *cl.map_shared_rank(&cnt, r);
+      if (r < rank) at += c;
+      total += c;
+    }
+    // this CTA's visible tiles, four a thread, in order
     int f[4], mine = 0;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int t = t0 + 4 * tid + x;
-      f[x] = t < tiles ? flags[t] : 0;
+      f[x] = 4 * tid + x < n ? flag[4 * tid + x] : 0;
       mine += f[x] != 0;
     }
     int incl = mine;
@@ -1186,17 +1281,15 @@ __global__ void __launch_bounds__(1024) paged_list_kernel(const __grid_constant_
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    int at = done + incl - mine;
-    for (int i = 0; i < 32; ++i) {
-      if (i < warp) at += wsum[i];
-      done += wsum[i];
-    }
+    for (int i = 0; i < warp; ++i) at += wsum[i];
+    at += incl - mine;
 #pragma unroll
     for (int x = 0; x < 4; ++x)
-      if (f[x]) list[at++] = ((t0 + 4 * tid + x) << 1) | (f[x] == 1);
-    __syncthreads();
+      if (f[x]) out.list[(int64_t)g * p.list_stride + at++] = ((t0 + a + 4 * tid + x) << 1) | (f[x] == 1);
+    done += total;
+    cl.sync();  // every CTA has read the counts, and this one's flags and sums are free again
   }
-  if (tid == 0) out.counts[g] = done;
+  if (rank == 0 && tid == 0) out.counts[g] = done;
 }
 
 }  // namespace
@@ -1235,18 +1328,13 @@ static cudaError_t launch_rows(const PagedAttnParams& p, const CUtensorMap& tk, 
 int paged_tile_keys(int d, int bits) { return bits == 16 && d == 128 ? 32 : 64; }
 
 cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                                   PlanOut plan, cudaStream_t st) {
+                                   const PlanOut& plan, cudaStream_t st) {
   if (p.list) {
-    plan.chunks = (p.list_stride + kPlanTiles - 1) / kPlanTiles;
-    if (plan.chunks > 0) {
-      const unsigned blocks = (unsigned)plan.chunks * p.n_groups;
-      note_launch();
-      if (p.tile_keys == 32) paged_plan_kernel<32><<<blocks, 256, 0, st>>>(p, plan);
-      else paged_plan_kernel<64><<<blocks, 256, 0, st>>>(p, plan);
-      const cudaError_t e = cudaGetLastError();
-      if (e != cudaSuccess) return e;
-    }
-    const cudaError_t e = launch_after(paged_list_kernel, dim3(p.n_groups), dim3(1024), 0, st, p, plan);
+    const unsigned blocks = (unsigned)p.n_groups * kPlanCtas;
+    note_launch();
+    if (p.tile_keys == 32) paged_plan_kernel<32><<<blocks, kPlanThreads, 0, st>>>(p, plan);
+    else paged_plan_kernel<64><<<blocks, kPlanThreads, 0, st>>>(p, plan);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   if (p.pg.d == 128) return p.pg.bits == 16 ? launch_rows<128, 16>(p, tk, tv, grid, st) : launch_rows<128, 4>(p, tk, tv, grid, st);

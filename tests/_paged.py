@@ -95,7 +95,9 @@ def attention(q, cache, lens, vec=(None,) * 4, start=None, causal=True, scale=No
     result once more: |do| <= 2^-8 sum w |v| + 2^-8 |o|.  With 4 bits the rounded weight multiplies scale * (code - 8)
     and the rest of the value is summed in fp32: |v| there is |scale (code - 8)|.  Scores are sums
     of d products in fp32, at most 2^-23 of sum |q k| a term, which moves each weight by twice delta
-    relatively; 2^-16 covers exp2, the running sums over the keys and the merge."""
+    relatively.  With 4 bits scale * (16 + code) is multiplied, from -24 scale sum(q) on: running sums of at most
+    55 scale sum |q|, rounded twice for every 16 products; sum(q) times minimum + 8 scale comes to it.  2^-16 covers
+    exp2, the running sums over the keys and the merge."""
     B, Nq, Hq, d = q.shape
     G = Hq // cache.Hkv
     scale = 1 / math.sqrt(d) if scale is None else scale
@@ -113,7 +115,8 @@ def attention(q, cache, lens, vec=(None,) * 4, start=None, causal=True, scale=No
             sk, sv = (np.stack([f64(s.cpu()[ids[j // cache.page], :, j % cache.page]) for j in range(n)])
                       for s in (cache.ks, cache.vs))
             mid_k, mid_v = (s[..., 1:] + 8 * s[..., :1] for s in (sk, sv))
-            size_k, size_v = np.abs(k - mid_k) + np.abs(mid_k), np.abs(v - mid_v)
+            size_k = (55 * d / 8 * sk[..., :1] / (d + 4) + np.abs(mid_k)) * np.ones(d)
+            size_v = np.abs(v - mid_v)
         first = n - Nq if start is None else int(start[b])
         for i in range(Nq):
             for h in range(Hq):
