@@ -61,7 +61,6 @@ struct PagedAttnParams {
   float* lse;
   // work: groups (a sequence, or a sequence and KV head with per-head masks) of `mult` items of `rows` rows
   int per_head, n_groups, mult, n_rb, rows, tile_keys;
-  int min_tiles;            // units that a run holds at least
   int mode;                 // kPaged*: how the work is divided
   // plan (with mask vectors): visible tiles of each group, row-visibility words of each key
   const int* counts;        // [n_groups]
@@ -78,10 +77,12 @@ struct PagedAttnParams {
   uint64_t wait_limit_ns;
 };
 
-// What the plan kernel writes: counts, list and words as above.
+// What the plan kernels write: counts, list and words as above, and the class of every tile
+// (0 no pair visible, 1 some pair hidden, 2 all visible), [n_groups, list_stride].
 struct PlanOut {
   int *counts, *list;
   uint32_t* words;
+  uint8_t* flags;
 };
 
 constexpr int kPagedMaxCtas = 160;

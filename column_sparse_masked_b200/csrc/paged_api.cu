@@ -79,14 +79,14 @@ int check_paged_rows(const flashmask_pages* pg, const flashmask_paged_rows* r) {
 
 // Work split and workspace of an attention call.
 struct PagedLayout {
-  int per_head, n_groups, mult, n_rb, rows, tile_keys, n_words, mode;
+  int masked, per_head, n_groups, mult, n_rb, rows, tile_keys, n_words, mode;
   int64_t keys;  // capacity of the table, in whole tiles
-  size_t part, stat, meta, counts, list, words, bytes;
+  size_t part, stat, meta, counts, list, words, flags, bytes;
 };
 
 PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& r) {
   PagedLayout L{};
-  const bool masked = r.lts || r.uts;
+  const bool masked = L.masked = (r.lts || r.uts) && pg.table_width > 0;
   const int64_t R = (int64_t)r.Nq * (r.Hq / pg.Hkv);
   L.rows = R <= 8 ? 8 : R <= 16 ? 16 : 32;
   L.n_rb = (int)((R + L.rows - 1) / L.rows);
@@ -115,6 +115,7 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
     L.counts = take((size_t)L.n_groups * 4);
     L.list = take((size_t)L.n_groups * (L.keys / L.tile_keys) * 4);
     L.words = take((size_t)pg.B * r.Hm * L.n_words * L.keys * 4);
+    L.flags = take((size_t)L.n_groups * (L.keys / L.tile_keys));
   }
   L.bytes = off > 0 ? off : 256;
   return L;
@@ -219,7 +220,7 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
   p.lte = r.lte;
   p.uts = r.uts;
   p.ute = r.ute;
-  const bool masked = r.lts || r.uts;
+  const bool masked = L.masked;
   p.Nq = r.Nq;
   p.Hq = r.Hq;
   p.Hm = masked ? r.Hm : 1;
@@ -236,7 +237,6 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
   p.n_rb = L.n_rb;
   p.rows = L.rows;
   p.tile_keys = L.tile_keys;
-  p.min_tiles = 2;
   p.mode = L.mode;
   p.part = reinterpret_cast<float*>(ws + L.part);
   p.stat = reinterpret_cast<float2*>(ws + L.stat);
@@ -246,6 +246,7 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
     p.counts = plan.counts = reinterpret_cast<int*>(ws + L.counts);
     p.list = plan.list = reinterpret_cast<int*>(ws + L.list);
     p.words = plan.words = reinterpret_cast<uint32_t*>(ws + L.words);
+    plan.flags = ws + L.flags;
     p.list_stride = (int)(L.keys / L.tile_keys);
     p.n_words = L.n_words;
     p.words_stride = L.keys;

@@ -33,7 +33,6 @@
 //      o   = sum (p s)(c - 8) + sum p (m + 8 s)
 //    The contraction may run over the head's values in any order as long as
 //    both sides agree, so each thread takes whole 16-byte pieces of code rows.
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -42,13 +41,12 @@
 #include "paged.cuh"
 #include "sm100_primitives.cuh"
 
-namespace cg = cooperative_groups;
-
 namespace fm {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kMetaInts = 8;
+constexpr int kMinTiles = 2;  // tiles that a run holds at least
 
 // ---------------------------------------------------------------------------
 // work: groups of items with the same number of tiles, and a CTA's run of units
@@ -71,16 +69,20 @@ __device__ __forceinline__ int key_bound(const PagedAttnParams& p, const Seq& q)
   return hi > 0 ? (int)hi : 0;
 }
 
-// The CTA's copy of the sequences (and, with lists, of the groups' tile
-// counts): once the rings are filled a load from memory waits behind them.
+__device__ __forceinline__ int load_tiles(const PagedAttnParams& p, int g) {
+  return p.counts ? p.counts[g] : (key_bound(p, load_seq(p, group_batch(p, g))) + p.tile_keys - 1) / p.tile_keys;
+}
+
+// The CTA's copy of the sequences and of the groups' tile counts: once the
+// rings are filled a load from memory waits behind them.
 constexpr int kSeqCache = 512;
 struct Seqs {
-  const Seq* seq;     // shared memory, or null: too many to hold
-  const int* counts;
-  __device__ __forceinline__ Seq get(const PagedAttnParams& p, int b) const { return seq ? seq[b] : load_seq(p, b); }
+  const Seq* seq;    // shared memory: the sequences (held: B <= kSeqCache)
+  const int* tiles_; // shared memory: tiles of the groups' items (held: n_groups <= kSeqCache)
+  bool has_seq, has_tiles;
+  __device__ __forceinline__ Seq get(const PagedAttnParams& p, int b) const { return has_seq ? seq[b] : load_seq(p, b); }
   __device__ __forceinline__ int tiles(const PagedAttnParams& p, int g) const {
-    if (p.counts) return counts ? counts[g] : p.counts[g];
-    return (key_bound(p, get(p, group_batch(p, g))) + p.tile_keys - 1) / p.tile_keys;
+    return has_tiles ? tiles_[g] : load_tiles(p, g);
   }
 };
 
@@ -116,10 +118,10 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const PagedAttnParams& p, int g, int in, int rows_per_item) {
   Item it;
+  const int kv = p.n_rb == 1 ? in : in / p.n_rb;
   it.b = group_batch(p, g);
-  const int rb = in % p.n_rb;
-  it.kvh = p.per_head ? g % p.pg.Hkv : in / p.n_rb;
-  it.row0 = rb * rows_per_item;
+  it.kvh = p.per_head ? g % p.pg.Hkv : kv;
+  it.row0 = (in - kv * p.n_rb) * rows_per_item;
   return it;
 }
 
@@ -212,6 +214,8 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map,
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(row)
       : "memory");
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // 16 bytes per lane, global to shared memory; a group of them is one tile.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -318,20 +322,24 @@ struct Issuer {
     more = true;
   }
 
+  // The next batch; false at the run's end.
+  __device__ __forceinline__ bool look_up(const PagedAttnParams& p, const Seqs& sq, int box_shift) {
+    if (!more) return false;
+    while (k >= w.n) {
+      k -= w.n;
+      if (!w.next(p, sq)) {
+        more = false;
+        x = nb = 0;
+        return false;
+      }
+    }
+    batch(p, sq, box_shift);
+    return true;
+  }
+
   __device__ __forceinline__ void issue(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
                                         const Smem<D, BITS, NT>& sm, const Seqs& sq, int warp, int box_shift) {
-    if (x == nb) {
-      if (!more) return;
-      while (k >= w.n) {
-        k -= w.n;
-        if (!w.next(p, sq)) {
-          more = false;
-          x = nb = 0;
-          return;
-        }
-      }
-      batch(p, sq, box_shift);
-    }
+    if (x == nb && !look_up(p, sq, box_shift)) return;
     const int lane = threadIdx.x & 31;
     const int tj = __shfl_sync(0xffffffffu, j0, x), f = __shfl_sync(0xffffffffu, flags, x);
     const int stage = warp * C::kDepth + issued % C::kDepth;
@@ -397,7 +405,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
   float qsum[2 * NT];
   uint2* qw = sm.q + warp * (C::kQBytes / 8);
   auto row_ptr = [&](const Item& it, int r) {
-    const int row = it.row0 + r, i = row / p.G;
+    const int row = it.row0 + r, i = p.Nq == 1 ? 0 : row / p.G;
     return p.q + it.b * p.qs[0] + i * p.qs[1] + (it.kvh * p.G + row - i * p.G) * p.qs[2];
   };
   auto load_q = [&](const Item& it) {
@@ -471,9 +479,12 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
   };
 
   Item it = item_of(p, wk.g, wk.in, C::kRows);
-  load_q(it);  // before the rings: what is loaded after them waits behind them
   Issuer<D, BITS, NT, STEP> is;
   is.start(wk, COOP ? warp : 0);
+  // before the rings: what is loaded after them waits behind them
+  load_q(it);
+  is.look_up(p, sq, box_shift);
+  turn_q(it);
 #pragma unroll 1
   for (int i = 0; i < C::kDepth; ++i) {
     is.issue(p, tk, tv, sm, sq, warp, box_shift);
@@ -486,10 +497,10 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
     if (!first_seg) {
       it = item_of(p, wk.g, wk.in, C::kRows);
       load_q(it);
+      turn_q(it);
     }
     const Seq seq = sq.get(p, it.b);
     const int R = p.Nq * p.G - it.row0;  // real rows of the block (may exceed kRows)
-    turn_q(it);
 
     float acc[MT][NT][4], mx[2 * NT], sum[2 * NT], cor[2 * NT];
 #pragma unroll
@@ -974,17 +985,30 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
   wc.limit_ns = p.wait_limit_ns;
   wc.smem_base = smem_addr(raw);
   wc.kernel = 5;
+  // Rows of Q and the page table towards the L2: a batch's keys have evicted them since the last call, and
+  // one run's chain of lengths, pages, rows and tiles would pay for each in turn.  (No value is read.)
+  {
+    const int n = p.pg.B * p.Nq * p.Hq, at = blockIdx.x * C::kThreads + tid, all = gridDim.x * C::kThreads;
+    for (int r = at; r < min(n, 2 * all); r += all) {
+      const int h = r % p.Hq, bi = r / p.Hq, b = bi / p.Nq;
+      prefetch_l2(p.q + b * p.qs[0] + (bi - b * p.Nq) * p.qs[1] + h * p.qs[2]);
+      if (D == 128) prefetch_l2(p.q + b * p.qs[0] + (bi - b * p.Nq) * p.qs[1] + h * p.qs[2] + 64);
+    }
+    const int lines = (p.pg.table_width + 31) / 32;
+    for (int r = at; r < min(p.pg.B * lines, 2 * all); r += all)
+      prefetch_l2(p.pg.table + (r / lines) * p.pg.table_stride + (r % lines) * 32);
+  }
   griddep_wait();
   griddep_launch_dependents();
-  Seqs sq{nullptr, nullptr};
-  if (p.pg.B <= kSeqCache) {
-    for (int b = tid; b < p.pg.B; b += C::kThreads) sm.seq[b] = load_seq(p, b);
-    sq.seq = sm.seq;
-  }
-  if (p.counts && p.n_groups <= kSeqCache) {
+  const Seqs sq{sm.seq, sm.counts, p.pg.B <= kSeqCache, p.n_groups <= kSeqCache};
+  if (sq.has_seq)
+    for (int b = tid; b < p.pg.B; b += C::kThreads) {
+      const Seq q = load_seq(p, b);
+      sm.seq[b] = q;
+      if (!p.counts && sq.has_tiles && !p.per_head) sm.counts[b] = (key_bound(p, q) + C::kKT - 1) / C::kKT;
+    }
+  if (p.counts && sq.has_tiles)
     for (int g = tid; g < p.n_groups; g += C::kThreads) sm.counts[g] = p.counts[g];
-    sq.counts = sm.counts;
-  }
   __syncthreads();
 
   Walk wk;
@@ -1025,7 +1049,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
   }
   const int total = __shfl_sync(0xffffffffu, incl, 31) * p.mult;
   // units of a run: total / workers, one more for the first total % workers
-  const int workers = min(all_workers, max(1, total / p.min_tiles)), q = total / workers, rem = total - q * workers;
+  const int workers = min(all_workers, max(1, total / kMinTiles)), q = total / workers, rem = total - q * workers;
   const int u0 = worker * q + min(worker, rem), n_units = worker < workers ? q + (worker < rem ? 1 : 0) : 0;
   if (lane == 0) p.meta[worker * kMetaInts] = -1;
   if (n_units > 0) {
@@ -1179,14 +1203,11 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
 }
 
 // ---------------------------------------------------------------------------
-// plan: row-visibility words and the list of visible tiles.  One cluster of 8
-// CTAs per group: each CTA reads an eighth of the group's mask vectors, one
-// warp per tile, and the CTAs exchange their counts through distributed shared
-// memory, so that one launch both reads the vectors with 256 warps and leaves
-// the list in order.
+// plan: row-visibility words and the class of every tile (one warp per tile),
+// then the list of visible tiles (one CTA per group).  A cluster of 8 CTAs per
+// group that does both in one launch took 30 us for one sequence of 128K keys:
+// 8 SMs do not have enough loads in flight for 2 MB of vectors.
 // ---------------------------------------------------------------------------
-constexpr int kPlanCtas = 8, kPlanThreads = 1024, kPlanTiles = 4096;  // tiles of one CTA at a time
-
 // Rows [p0, p0 + 32) with [lo, hi) cut out, as a word.
 __device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t p0) {
   const int a = (int)min(max(lo - p0, (int64_t)0), (int64_t)32), b = (int)min(max(hi - p0, (int64_t)0), (int64_t)32);
@@ -1194,83 +1215,76 @@ __device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t p0) 
 }
 
 template <int KT>
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    paged_plan_kernel(const __grid_constant__ PagedAttnParams p, PlanOut out) {
-  __shared__ uint8_t flag[kPlanTiles];
-  __shared__ int cnt, wsum[32];
+__global__ void __launch_bounds__(256) paged_plan_kernel(const __grid_constant__ PagedAttnParams p, PlanOut out) {
+  griddep_wait();
   griddep_launch_dependents();
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank(), g = blockIdx.x / kPlanCtas;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, x = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int g = x / p.list_stride, t = x - g * p.list_stride;
+  if (g >= p.n_groups) return;
   const int b = group_batch(p, g);
   const int hm0 = p.per_head ? (g % p.pg.Hkv) * p.G : 0, nh = p.per_head ? p.G : 1;
   const Seq seq = load_seq(p, b);
-  const int hi = key_bound(p, seq), tiles = (hi + KT - 1) / KT;
-  int done = 0;
-  for (int t0 = 0; t0 < tiles; t0 += kPlanCtas * kPlanTiles) {
-    const int block = min(tiles - t0, kPlanCtas * kPlanTiles), share = (block + kPlanCtas - 1) / kPlanCtas;
-    const int a = min(rank * share, block), n = min(share, block - a);  // this CTA's tiles: t0 + a + [0, n)
-    int seen = 0;
-#pragma unroll 2
-    for (int t = warp; t < n; t += 32) {
-      bool any = false, all = true;
+  const int hi = key_bound(p, seq);
+  if (t * KT >= hi) return;
+  bool any = false, all = true;
+  for (int h = 0; h < nh; ++h) {
+    const int64_t at = ((int64_t)b * p.Hm + hm0 + h);
+    int4 v[KT / 32];
 #pragma unroll
-      for (int jj = 0; jj < KT; jj += 32) {
-        const int j = (t0 + a + t) * KT + jj + lane;
-        for (int h = 0; h < nh; ++h) {
-          const int64_t at = ((int64_t)b * p.Hm + hm0 + h);
-          int lts = 0, lte = 0, uts = 0, ute = 0;
-          if (j < p.Nm && j < hi) {
-            const int64_t m = at * p.Nm + j;
-            if (p.lts) {
-              lts = p.lts[m];
-              lte = p.lte[m];
-            }
-            if (p.uts) {
-              uts = p.uts[m];
-              ute = p.ute[m];
-            }
-          }
-          for (int w = 0; w < p.n_words; ++w) {
-            const int64_t p0 = (int64_t)seq.first + 32 * w;
-            const uint32_t rows = bit_range(0, min(32, p.Nq - 32 * w));
-            uint32_t see = 0;
-            if (j < hi) {
-              uint32_t hid = rows_in(lts, lte, p0) | rows_in(uts, ute, p0);
-              if (p.causal) hid |= rows_in(p0, j, p0);
-              see = rows & ~hid;
-            }
-            out.words[(at * p.n_words + w) * p.words_stride + j] = see;
-            any |= see != 0;
-            all &= see == rows;
-          }
+    for (int y = 0; y < KT / 32; ++y) {
+      const int j = t * KT + y * 32 + lane;
+      const int64_t m = at * p.Nm + j;
+      v[y] = make_int4(0, 0, 0, 0);
+      if (j < p.Nm && j < hi) {
+        if (p.lts) {
+          v[y].x = p.lts[m];
+          v[y].y = p.lte[m];
+        }
+        if (p.uts) {
+          v[y].z = p.uts[m];
+          v[y].w = p.ute[m];
         }
       }
-      any = __any_sync(0xffffffffu, any);
-      all = __all_sync(0xffffffffu, all);
-      if (lane == 0) flag[t] = any ? (all ? 2 : 1) : 0;
-      seen += any;
     }
-    if (lane == 0) wsum[warp] = seen;
-    __syncthreads();
-    if (warp == 0) {
-      int v = wsum[lane];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) cnt = v;
+    for (int y = 0; y < KT / 32; ++y) {
+      const int j = t * KT + y * 32 + lane;
+      for (int w = 0; w < p.n_words; ++w) {
+        const int64_t p0 = (int64_t)seq.first + 32 * w;
+        const uint32_t rows = bit_range(0, min(32, p.Nq - 32 * w));
+        uint32_t see = 0;
+        if (j < hi) {
+          uint32_t hid = rows_in(v[y].x, v[y].y, p0) | rows_in(v[y].z, v[y].w, p0);
+          if (p.causal) hid |= rows_in(p0, j, p0);
+          see = rows & ~hid;
+        }
+        out.words[(at * p.n_words + w) * p.words_stride + j] = see;
+        any |= see != 0;
+        all &= see == rows;
+      }
     }
-    cl.sync();
-    int at = done, total = 0;
-    for (int r = 0; r < kPlanCtas; ++r) {
-      const int c = *cl.map_shared_rank(&cnt, r);
-      if (r < rank) at += c;
-      total += c;
-    }
-    // this CTA's visible tiles, four a thread, in order
+  }
+  any = __any_sync(0xffffffffu, any);
+  all = __all_sync(0xffffffffu, all);
+  if (lane == 0) out.flags[x] = any ? (all ? 2 : 1) : 0;
+}
+
+__global__ void __launch_bounds__(1024) paged_list_kernel(const __grid_constant__ PagedAttnParams p, PlanOut out) {
+  __shared__ int wsum[32];
+  const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hi = key_bound(p, load_seq(p, group_batch(p, g)));  // the call's inputs, not the plan's
+  const int tiles = (hi + p.tile_keys - 1) / p.tile_keys;
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint8_t* flags = out.flags + (int64_t)g * p.list_stride;
+  int* list = out.list + (int64_t)g * p.list_stride;
+  int done = 0;
+  for (int t0 = 0; t0 < tiles; t0 += 4096) {  // four tiles a thread at a time
     int f[4], mine = 0;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      f[x] = 4 * tid + x < n ? flag[4 * tid + x] : 0;
+      const int t = t0 + 4 * tid + x;
+      f[x] = t < tiles ? flags[t] : 0;
       mine += f[x] != 0;
     }
     int incl = mine;
@@ -1281,15 +1295,20 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    for (int i = 0; i < warp; ++i) at += wsum[i];
-    at += incl - mine;
+    int v = wsum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    int at = done + incl - mine + (warp > 0 ? __shfl_sync(0xffffffffu, v, (warp - 1) & 31) : 0);
+    done += __shfl_sync(0xffffffffu, v, 31);
 #pragma unroll
     for (int x = 0; x < 4; ++x)
-      if (f[x]) out.list[(int64_t)g * p.list_stride + at++] = ((t0 + a + 4 * tid + x) << 1) | (f[x] == 1);
-    done += total;
-    cl.sync();  // every CTA has read the counts, and this one's flags and sums are free again
+      if (f[x]) list[at++] = ((t0 + 4 * tid + x) << 1) | (f[x] == 1);
+    __syncthreads();
   }
-  if (rank == 0 && tid == 0) out.counts[g] = done;
+  if (tid == 0) out.counts[g] = done;
 }
 
 }  // namespace
@@ -1329,12 +1348,14 @@ int paged_tile_keys(int d, int bits) { return bits == 16 && d == 128 ? 32 : 64; 
 
 cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                                    const PlanOut& plan, cudaStream_t st) {
-  if (p.list) {
-    const unsigned blocks = (unsigned)p.n_groups * kPlanCtas;
+  if (p.list && p.list_stride > 0) {
+    const unsigned blocks = (unsigned)(((int64_t)p.n_groups * p.list_stride + 7) / 8);
     note_launch();
-    if (p.tile_keys == 32) paged_plan_kernel<32><<<blocks, kPlanThreads, 0, st>>>(p, plan);
-    else paged_plan_kernel<64><<<blocks, kPlanThreads, 0, st>>>(p, plan);
-    const cudaError_t e = cudaGetLastError();
+    if (p.tile_keys == 32) paged_plan_kernel<32><<<blocks, 256, 0, st>>>(p, plan);
+    else paged_plan_kernel<64><<<blocks, 256, 0, st>>>(p, plan);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_after(paged_list_kernel, dim3(p.n_groups), dim3(1024), 0, st, p, plan);
     if (e != cudaSuccess) return e;
   }
   if (p.pg.d == 128) return p.pg.bits == 16 ? launch_rows<128, 16>(p, tk, tv, grid, st) : launch_rows<128, 4>(p, tk, tv, grid, st);

@@ -315,6 +315,9 @@ def test_attention_empty_calls():
     none = torch.zeros(1, 0, dtype=torch.int32, device="cuda")
     o, lse = fm.paged_attention(case_q(1, 2, 4, 64), cache.k[:0], cache.v[:0], none, i32([0]))
     assert (o == 0).all() and torch.isneginf(lse).all()
+    m = torch.zeros(1, 4, 9, dtype=torch.int32, device="cuda")
+    o, lse = fm.paged_attention(case_q(1, 2, 4, 64), cache.k, cache.v, none, i32([0]), m, m)
+    assert (o == 0).all() and torch.isneginf(lse).all()
 
 
 # ---------------------------------------------------------------------------
