@@ -72,8 +72,9 @@ int check_paged_rows(const flashmask_pages* pg, const flashmask_paged_rows* r) {
   }
   // work items are numbered in 32 bits
   if ((int64_t)pg->B * r->Nq * r->Hq > INT_MAX / 4) return FLASHMASK_ERR_UNSUPPORTED;
-  const int64_t tiles = ((int64_t)pg->table_width * pg->page_size + 31) / 32, blocks = ((int64_t)r->Nq * (r->Hq / pg->Hkv) + 7) / 8;
-  if (blocks * pg->Hkv * pg->B > INT_MAX / 2 / (tiles > 0 ? tiles : 1)) return FLASHMASK_ERR_UNSUPPORTED;
+  const int64_t units = ((int64_t)pg->table_width * pg->page_size + 31) / 32 + 2;
+  const int64_t blocks = ((int64_t)r->Nq * (r->Hq / pg->Hkv) + 7) / 8;
+  if (blocks * pg->Hkv * pg->B > INT_MAX / 2 / units) return FLASHMASK_ERR_UNSUPPORTED;
   return FLASHMASK_OK;
 }
 

@@ -46,7 +46,7 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kMetaInts = 8;
-constexpr int kMinTiles = 2;  // tiles that a run holds at least
+constexpr int kMinUnits = 4;  // units that a run holds at least (kItemCost of them may stand for an item)
 
 // ---------------------------------------------------------------------------
 // work: groups of items with the same number of tiles, and a CTA's run of units
@@ -87,30 +87,52 @@ struct Seqs {
 };
 
 // A run, walked segment by segment (a segment: tiles [t, t + n) of one item).
-// Runs are made of units (tiles), or of whole items.
+// Runs are made of units, or of whole items.  An item has a unit for each of
+// its tiles and kItemCost units before them, which stand for what an item
+// costs besides (rows of Q, pages, output): a run of many short items would
+// end late without them.
+constexpr int kItemCost = 2;
 struct Walk {
-  int g, in, t, T;  // group, item in the group, first tile, tiles of the group's items
-  int left;         // units (items) left in the run
-  int n;            // tiles of this segment
-  __device__ __forceinline__ bool next(const PagedAttnParams& p, const Seqs& sq) {
-    left -= p.mode == kPagedSplit ? n : 1;
-    if (left <= 0) return false;
-    t = 0;
-    if (++in == p.mult) {
-      in = 0;
-      do {
-        ++g;
-        T = sq.tiles(p, g);
-      } while (T == 0 && p.mode == kPagedSplit);
+  int g, in, T;   // group, item in the group, tiles of the group's items
+  int pos, left;  // unit of the item that the segment begins at; units (items) left in the run
+  int base;       // number of the item's first unit
+  int t, n;       // first tile and tiles of the segment
+  __device__ __forceinline__ void cut(const PagedAttnParams& p) {
+    if (p.mode != kPagedSplit) {
+      t = 0;
+      n = T;
+    } else {
+      t = max(pos - kItemCost, 0);
+      n = max(min(T + kItemCost, pos + left) - kItemCost, 0) - t;
     }
-    n = p.mode == kPagedSplit ? min(T, left) : T;
+  }
+  // The next segment that has tiles (of whole items: the next item); false at the run's end.
+  __device__ __forceinline__ bool next(const PagedAttnParams& p, const Seqs& sq) {
+    do {
+      left -= p.mode == kPagedSplit ? T + kItemCost - pos : 1;
+      if (left <= 0) return false;
+      base += T + kItemCost;
+      pos = 0;
+      if (++in == p.mult) {
+        in = 0;
+        do {
+          ++g;
+          T = sq.tiles(p, g);
+        } while (T == 0 && p.mode == kPagedSplit);
+      }
+      cut(p);
+    } while (n <= 0 && p.mode == kPagedSplit);
     return true;
+  }
+  __device__ __forceinline__ bool first(const PagedAttnParams& p, const Seqs& sq) {
+    cut(p);
+    return n > 0 || p.mode != kPagedSplit || next(p, sq);
   }
 };
 
-// A warp's run of units: [u0, u0 + ...), one of runs of q units, one more for the first rem.
+// A warp's run: one of runs of q units, one more for the first rem.
 struct Run {
-  int worker, u0, q, rem;
+  int worker, q, rem;
 };
 
 struct Item {
@@ -322,24 +344,18 @@ struct Issuer {
     more = true;
   }
 
-  // The next batch; false at the run's end.
-  __device__ __forceinline__ bool look_up(const PagedAttnParams& p, const Seqs& sq, int box_shift) {
-    if (!more) return false;
-    while (k >= w.n) {
+  // The next batch, if the run has more tiles.
+  __device__ __forceinline__ void look_up(const PagedAttnParams& p, const Seqs& sq, int box_shift) {
+    x = nb = 0;
+    while (more && k >= w.n) {
       k -= w.n;
-      if (!w.next(p, sq)) {
-        more = false;
-        x = nb = 0;
-        return false;
-      }
+      more = w.next(p, sq);
     }
-    batch(p, sq, box_shift);
-    return true;
+    if (more) batch(p, sq, box_shift);
   }
 
   __device__ __forceinline__ void issue(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
-                                        const Smem<D, BITS, NT>& sm, const Seqs& sq, int warp, int box_shift) {
-    if (x == nb && !look_up(p, sq, box_shift)) return;
+                                        const Smem<D, BITS, NT>& sm, int warp, int box_shift) {
     const int lane = threadIdx.x & 31;
     const int tj = __shfl_sync(0xffffffffu, j0, x), f = __shfl_sync(0xffffffffu, flags, x);
     const int stage = warp * C::kDepth + issued % C::kDepth;
@@ -478,31 +494,28 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
     }
   };
 
-  Item it = item_of(p, wk.g, wk.in, C::kRows);
   Issuer<D, BITS, NT, STEP> is;
   is.start(wk, COOP ? warp : 0);
-  // before the rings: what is loaded after them waits behind them
-  load_q(it);
-  is.look_up(p, sq, box_shift);
-  turn_q(it);
-#pragma unroll 1
-  for (int i = 0; i < C::kDepth; ++i) {
-    is.issue(p, tk, tv, sm, sq, warp, box_shift);
-    if (BITS == 4) copy_commit();
-  }
-  int k = COOP ? warp : 0, taken = 0;  // the warp's next tile in the segment, and the tiles it has taken
-  bool alive = true, first_seg = true;
-  int u = run.u0;  // first unit of the segment
-  do {
-    if (!first_seg) {
+  Item it{};
+  Seq seq{};
+  int R = 0;                          // real rows of the block (may exceed kRows)
+  int k = COOP ? warp : 0;            // the warp's next tile in the segment
+  int ahead = 0, taken = 0;           // tiles in the ring, and tiles taken out of it
+  bool alive = true, fresh = true, first_seg = true;
+  float acc[MT][NT][4], mx[2 * NT], sum[2 * NT], cor[2 * NT];
+  // One loop for all tiles of the run, with one place each that loads rows, looks pages up, fills the
+  // ring and works on a tile: the instruction cache is cold at every launch.
+  for (;;) {
+    if (fresh) {
       it = item_of(p, wk.g, wk.in, C::kRows);
       load_q(it);
-      turn_q(it);
     }
-    const Seq seq = sq.get(p, it.b);
-    const int R = p.Nq * p.G - it.row0;  // real rows of the block (may exceed kRows)
-
-    float acc[MT][NT][4], mx[2 * NT], sum[2 * NT], cor[2 * NT];
+    if (is.x == is.nb) is.look_up(p, sq, box_shift);
+    if (fresh) {
+      turn_q(it);
+      seq = sq.get(p, it.b);
+      R = p.Nq * p.G - it.row0;
+      fresh = false;
 #pragma unroll
     for (int x = 0; x < 2 * NT; ++x) {
       mx[x] = -INFINITY;
@@ -516,17 +529,23 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
 
-    for (; k < wk.n; k += STEP) {
-      const int stage = warp * C::kDepth + taken % C::kDepth;
-      if (BITS == 16) {
-        if (alive) alive = mbar_wait(&sm.full[stage], (taken / C::kDepth) & 1u, wc);
-        alive = __all_sync(0xffffffffu, alive);
-        if (!alive) continue;
-      } else {
-        copy_wait<C::kDepth - 1>();
+    }
+    const int stage = warp * C::kDepth + taken % C::kDepth;
+    if (BITS == 16 && ahead > 0 && k < wk.n) {
+      if (alive) alive = mbar_wait(&sm.full[stage], (taken / C::kDepth) & 1u, wc);
+      alive = __all_sync(0xffffffffu, alive);
+      if (!alive)  // gave up: walks to the run's end
+        while (k < wk.n) k += STEP;
+    }
+    if (ahead > 0 && k < wk.n) {
+      if (BITS == 4) {
+        if (ahead == C::kDepth) copy_wait<C::kDepth - 1>();
+        else copy_wait<0>();
         __syncwarp();
       }
       ++taken;
+      --ahead;
+      k += STEP;
       const int4 hd = sm.hdr[stage];
       uint8_t* st = sm.stage + stage * C::kStage;
       const uint32_t kaddr = smem_addr(st), vaddr = kaddr + C::kHalf;
@@ -798,10 +817,16 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
       }
       if (BITS == 16 && wrote) fence_async_smem();
       __syncwarp();
-      is.issue(p, tk, tv, sm, sq, warp, box_shift);
-      if (BITS == 4) copy_commit();  // a group per tile, empty at the run's end
     }
+    while (ahead < C::kDepth && is.x < is.nb && alive) {
+      is.issue(p, tk, tv, sm, warp, box_shift);
+      if (BITS == 4) copy_commit();
+      ++ahead;
+    }
+    if (k < wk.n) continue;
     k -= wk.n;
+
+    // ---- the segment's end ----
 
 #pragma unroll
     for (int x = 0; x < 2 * NT; ++x) {
@@ -914,7 +939,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
       // ---- part of an item: sums and running maximum ----
       const int slot = 2 * run.worker + (first_seg ? 0 : 1);
       if (wk.t == 0 && lane == 0) {  // it begins here and goes on in the next runs: where its parts are
-        const int last = u + wk.T - 1, big = run.rem * (run.q + 1);  // the run that ends it holds unit `last`
+        const int last = wk.base + wk.T + kItemCost - 1, big = run.rem * (run.q + 1);  // the run that ends it holds unit `last`
         int* meta = p.meta + run.worker * kMetaInts;
         meta[0] = it.b;
         meta[1] = it.kvh;
@@ -944,8 +969,9 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
       }
     }
     first_seg = false;
-    u += wk.n;
-  } while (wk.next(p, sq));
+    if (!wk.next(p, sq)) break;
+    fresh = true;
+  }
   if (BITS == 16 && !alive && lane == 0) {  // gave up: let the copies in flight land before the CTA ends
     WaitCtx w2 = wc;
     int zero = 0;
@@ -1012,68 +1038,68 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
   __syncthreads();
 
   Walk wk;
-  if (COOP) {  // one item per CTA
-    wk.g = blockIdx.x / p.mult;
-    wk.in = blockIdx.x % p.mult;
-    wk.t = 0;
-    wk.T = wk.n = sq.tiles(p, wk.g);
-    wk.left = 1;
-    attend<D, BITS, NT, true>(p, &tk, &tv, sm, sq, wk, wc, Run{});
-    return;
-  }
+  Run run{};
+  bool works = true;
   // neighbouring runs go to different SMs: a small problem's few runs are spread over the device
   const int worker = warp * gridDim.x + blockIdx.x, all_workers = C::kWarps * gridDim.x;
-  if (p.mode == kPagedWhole) {
-    const int items = p.n_groups * p.mult, q = items / all_workers, rem = items - q * all_workers;
-    const int first = worker * q + min(worker, rem);
-    wk.left = q + (worker < rem ? 1 : 0);
-    if (wk.left == 0) return;
-    wk.g = first / p.mult;
-    wk.in = first % p.mult;
-    wk.t = 0;
-    wk.T = wk.n = sq.tiles(p, wk.g);
-    attend<D, BITS, NT, false>(p, &tk, &tv, sm, sq, wk, wc, Run{});
-    return;
-  }
-
-  // ---- every warp sums the groups' tiles and finds the group that its run begins in ----
-  const int per = (p.n_groups + 31) / 32, ga = min(lane * per, p.n_groups), gb = min(ga + per, p.n_groups);
-  int mine = 0;
-#pragma unroll 4
-  for (int g = ga; g < gb; ++g) mine += sq.tiles(p, g);
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  const int total = __shfl_sync(0xffffffffu, incl, 31) * p.mult;
-  // units of a run: total / workers, one more for the first total % workers
-  const int workers = min(all_workers, max(1, total / kMinTiles)), q = total / workers, rem = total - q * workers;
-  const int u0 = worker * q + min(worker, rem), n_units = worker < workers ? q + (worker < rem ? 1 : 0) : 0;
-  if (lane == 0) p.meta[worker * kMetaInts] = -1;
-  if (n_units > 0) {
-    const unsigned has = __ballot_sync(0xffffffffu, u0 < incl * p.mult);
-    const int src = __ffs(has) - 1;
-    int at = (incl - mine) * p.mult;
-    wk.g = ga;
-    wk.T = 0;
-    if (lane == src) {
-      wk.T = sq.tiles(p, wk.g);
-      while (u0 >= at + wk.T * p.mult) {
-        at += wk.T * p.mult;
-        wk.T = sq.tiles(p, ++wk.g);
-      }
+  if (COOP || p.mode == kPagedWhole) {  // whole items: one per CTA, or an equal share of them per warp
+    int first = blockIdx.x;
+    wk.left = 1;
+    if (!COOP) {
+      const int items = p.n_groups * p.mult, q = items / all_workers, rem = items - q * all_workers;
+      first = worker * q + min(worker, rem);
+      wk.left = q + (worker < rem ? 1 : 0);
+      works = wk.left > 0;
     }
-    wk.g = __shfl_sync(0xffffffffu, wk.g, src);
-    wk.T = __shfl_sync(0xffffffffu, wk.T, src);
-    const int off = u0 - __shfl_sync(0xffffffffu, at, src);
-    wk.in = off / wk.T;
-    wk.t = off - wk.in * wk.T;
-    wk.left = n_units;
-    wk.n = min(wk.T - wk.t, n_units);
-    attend<D, BITS, NT, false>(p, &tk, &tv, sm, sq, wk, wc, Run{worker, u0, q, rem});
+    wk.g = works ? first / p.mult : 0;
+    wk.in = first - wk.g * p.mult;
+    wk.T = sq.tiles(p, wk.g);
+    wk.pos = wk.base = 0;
+  } else {
+    // every warp sums the groups' units and finds the group that its run begins in
+    const int per = (p.n_groups + 31) / 32, ga = min(lane * per, p.n_groups), gb = min(ga + per, p.n_groups);
+    auto units = [&](int g) {
+      const int T = sq.tiles(p, g);
+      return T > 0 ? (T + kItemCost) * p.mult : 0;
+    };
+    int mine = 0;
+    for (int g = ga; g < gb; ++g) mine += units(g);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    // units of a run: total / workers, one more for the first total % workers
+    const int workers = min(all_workers, max(1, total / kMinUnits));
+    run.worker = worker;
+    run.q = total / workers;
+    run.rem = total - run.q * workers;
+    const int u0 = worker * run.q + min(worker, run.rem);
+    wk.left = worker < workers ? run.q + (worker < run.rem ? 1 : 0) : 0;
+    works = wk.left > 0;
+    if (lane == 0) p.meta[worker * kMetaInts] = -1;
+    if (works) {
+      const int src = __ffs(__ballot_sync(0xffffffffu, u0 < incl)) - 1;
+      int at = incl - mine, g = ga;
+      if (lane == src)
+        for (int n = units(g); u0 >= at + n; n = units(g)) {
+          at += n;
+          ++g;
+        }
+      wk.g = __shfl_sync(0xffffffffu, g, src);
+      wk.T = sq.tiles(p, wk.g);
+      const int off = u0 - __shfl_sync(0xffffffffu, at, src);
+      wk.in = off / (wk.T + kItemCost);
+      wk.pos = off - wk.in * (wk.T + kItemCost);
+      wk.base = u0 - wk.pos;
+      works = wk.first(p, sq);
+    }
   }
+  if (COOP || p.mode == kPagedWhole) wk.cut(p);
+  if (works) attend<D, BITS, NT, COOP>(p, &tk, &tv, sm, sq, wk, wc, run);
+  if (COOP || p.mode == kPagedWhole) return;
   for (int g = blockIdx.x; g < p.n_groups; g += gridDim.x)
     if (sq.tiles(p, g) == 0) write_empty<D>(p, g, C::kThreads);
 }
