@@ -1105,126 +1105,125 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// joining the parts of cut items: a warp per run and row where they are few,
-// the CTA together where they are many
+// joining the parts of cut items, in the order of their runs: a warp per item
+// and row where the parts are few, the CTA's 8 warps together where they are
+// many.  Latency is all it costs: the parts' values are asked for before their
+// weights are known.
 // ---------------------------------------------------------------------------
+struct Joined {
+  float m, l;
+  float4 o;
+};
+
+// Parts k0, k0 + step, ... of an item's row (a warp's lanes hold 4 values each, D/4 of them a part).
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int workers) {
-  constexpr int LG = D / 4, PP = 32 / LG;  // lanes of a row, parts that a warp reads at a time
-  __shared__ float red[8], wts[256];
-  __shared__ int metas[8][kMetaInts];
-  __shared__ float4 buf[8][32];
-  griddep_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
-  const int d4 = lane % LG, sub = lane / LG;
-  auto store = [&](const int* meta, float4 o, float top, float L) {
-    const int row = meta[2] + r, i = row / p.G, h = meta[1] * p.G + row % p.G;
-    const float inv = top == -INFINITY ? 0.f : 1.f / L;
-    *reinterpret_cast<uint2*>(p.o + (((int64_t)meta[0] * p.Nq + i) * p.Hq + h) * D + 4 * d4) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (d4 == 0)
-      p.lse[((int64_t)meta[0] * p.Hq + h) * p.Nq + i] =
-          top == -INFINITY ? -INFINITY : fmaf(top, p.scale_log2, log2f(L)) * kLn2;
-  };
-  auto add = [&](float4& o, int slot, float w) {
-    if (w == 0.f) return;  // a part that saw nothing
-    const float4 v = *reinterpret_cast<const float4*>(p.part + ((int64_t)slot * ROWS + r) * D + 4 * d4);
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
-  };
-  auto fold = [&](float4& o) {  // the sub-groups of a warp
-    if (PP == 2) {
-      o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
-      o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
-      o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
-      o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
-    }
-  };
-  const int v0 = blockIdx.x * 8;
-  if (tid < 8 * kMetaInts) {
-    const int v = v0 + tid / kMetaInts;
-    metas[tid / kMetaInts][tid % kMetaInts] = v < workers ? p.meta[v0 * kMetaInts + tid] : -1;
-  }
-  __syncthreads();
-  auto parts_of = [&](int x) { return metas[x][0] < 0 || metas[x][2] + r >= p.Nq * p.G ? 0 : metas[x][3] - (v0 + x) + 1; };
-  {
-    const int v = v0 + warp, parts = parts_of(warp);
-    if (parts > 0 && parts <= 32) {
-      const int* meta = metas[warp];
-      const int slot = 2 * (v + lane) + (lane == 0 ? meta[4] : 0);
-      const float2 ml = lane < parts ? p.stat[slot * ROWS + r] : make_float2(-INFINITY, 0.f);
-      float top = ml.x;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float w = ml.x == -INFINITY ? 0.f : fast_exp2((ml.x - top) * p.scale_log2);
-      float L = ml.y * w;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int k = 0; k < parts; k += PP) {
-        const int kk = k + sub;
-        const float wk = __shfl_sync(0xffffffffu, w, kk & 31);
-        const int sl = __shfl_sync(0xffffffffu, slot, kk & 31);
-        if (kk < parts) add(o, sl, wk);
-      }
-      fold(o);
-      if (sub == 0) store(meta, o, top, L);
-    }
-  }
-  for (int x = 0; x < 8; ++x) {
-    const int v = v0 + x, parts = parts_of(x);
-    if (parts <= 32) continue;
-    const int* meta = metas[x];
-    auto slot_of = [&](int k) { return 2 * (v + k) + (k == 0 ? meta[4] : 0); };
-    float top = -INFINITY;
-    for (int k = tid; k < parts; k += 256) top = fmaxf(top, p.stat[slot_of(k) * ROWS + r].x);
+__device__ __forceinline__ Joined join(const PagedAttnParams& p, int run, int first_slot, int parts, int k0, int step,
+                                       int r) {
+  constexpr int LG = D / 4, PP = 32 / LG;  // lanes of a part, parts that a warp reads at a time
+  const int lane = threadIdx.x & 31, d4 = lane % LG, sub = lane / LG;
+  auto slot = [&](int k) { return 2 * (run + k) + (k == 0 ? first_slot : 0); };
+  Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int base = k0; base < parts; base += 32 * step) {
+    const int mine = base + lane * step, n = min(32, (parts - base + step - 1) / step);
+    const float2 ml = mine < parts ? p.stat[slot(mine) * ROWS + r] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    __syncthreads();
-    if (lane == 0) red[warp] = top;
-    __syncthreads();
+    top = fmaxf(top, j.m);
+    const float f = j.m == -INFINITY ? 0.f : fast_exp2((j.m - top) * p.scale_log2);
+    const float w = ml.x == -INFINITY ? 0.f : fast_exp2((ml.x - top) * p.scale_log2);
+    float l = ml.y * w;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, red[i]);
-    float L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < parts; k0 += 256) {
-      __syncthreads();
-      float w = 0.f;
-      if (k0 + tid < parts) {
-        const float2 ml = p.stat[slot_of(k0 + tid) * ROWS + r];
-        w = ml.x == -INFINITY ? 0.f : fast_exp2((ml.x - top) * p.scale_log2);
-        L = fmaf(ml.y, w, L);
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    j.m = top;
+    j.l = fmaf(j.l, f, l);
+    j.o.x *= f;
+    j.o.y *= f;
+    j.o.z *= f;
+    j.o.w *= f;
+    for (int i0 = 0; i0 < n; i0 += 8 * PP) {
+      float4 v[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int i = i0 + x * PP + sub;
+        v[x] = i < n ? *reinterpret_cast<const float4*>(p.part + ((int64_t)slot(base + i * step) * ROWS + r) * D + 4 * d4)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      wts[tid] = w;
-      __syncthreads();
-      const int m = min(256, parts - k0);
-#pragma unroll 4
-      for (int k = warp * PP + sub; k < m; k += 8 * PP) add(o, slot_of(k0 + k), wts[k]);
-    }
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
-    fold(o);
-    __syncthreads();
-    if (lane == 0) red[warp] = L;
-    buf[warp][lane] = o;
-    __syncthreads();
-    if (warp == 0) {
-      L = 0.f;
-      o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        L += red[i];
-        const float4 b = buf[i][lane];
-        o.x += b.x;
-        o.y += b.y;
-        o.z += b.z;
-        o.w += b.w;
+      for (int x = 0; x < 8; ++x) {
+        const float wx = __shfl_sync(0xffffffffu, w, (i0 + x * PP + sub) & 31);
+        if (i0 + x * PP + sub < n && wx != 0.f) {  // 0: a part that saw nothing
+          j.o.x = fmaf(wx, v[x].x, j.o.x);
+          j.o.y = fmaf(wx, v[x].y, j.o.y);
+          j.o.z = fmaf(wx, v[x].z, j.o.z);
+          j.o.w = fmaf(wx, v[x].w, j.o.w);
+        }
       }
-      if (sub == 0) store(meta, o, top, L);
     }
+  }
+  if (PP == 2) {
+    j.o.x += __shfl_xor_sync(0xffffffffu, j.o.x, 16);
+    j.o.y += __shfl_xor_sync(0xffffffffu, j.o.y, 16);
+    j.o.z += __shfl_xor_sync(0xffffffffu, j.o.z, 16);
+    j.o.w += __shfl_xor_sync(0xffffffffu, j.o.w, 16);
+  }
+  return j;
+}
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int workers) {
+  __shared__ int metas[8][kMetaInts];
+  __shared__ float ms[8], ls[8];
+  __shared__ float4 os[8][32];
+  griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y, v0 = blockIdx.x * 8;
+  if (tid < 8 * kMetaInts)
+    metas[tid / kMetaInts][tid % kMetaInts] = v0 + tid / kMetaInts < workers ? p.meta[v0 * kMetaInts + tid] : -1;
+  __syncthreads();
+  auto store = [&](const int* meta, const Joined& j) {
+    const int row = meta[2] + r, i = row / p.G, h = meta[1] * p.G + row - i * p.G, d4 = lane % (D / 4);
+    const float inv = j.m == -INFINITY ? 0.f : 1.f / j.l;
+    if (lane >= D / 4) return;
+    *reinterpret_cast<uint2*>(p.o + (((int64_t)meta[0] * p.Nq + i) * p.Hq + h) * D + 4 * d4) =
+        make_uint2(pack_bf16x2(j.o.x * inv, j.o.y * inv), pack_bf16x2(j.o.z * inv, j.o.w * inv));
+    if (d4 == 0)
+      p.lse[((int64_t)meta[0] * p.Hq + h) * p.Nq + i] =
+          j.m == -INFINITY ? -INFINITY : fmaf(j.m, p.scale_log2, log2f(j.l)) * kLn2;
+  };
+  auto parts_of = [&](int x) { return metas[x][0] < 0 || metas[x][2] + r >= p.Nq * p.G ? 0 : metas[x][3] - (v0 + x) + 1; };
+  {
+    const int parts = parts_of(warp);
+    if (parts > 0 && parts <= 16)
+      store(metas[warp], join<D, ROWS>(p, v0 + warp, metas[warp][4], parts, 0, 1, r));
+  }
+  for (int x = 0; x < 8; ++x) {
+    const int parts = parts_of(x);
+    if (parts <= 16) continue;
+    Joined j = join<D, ROWS>(p, v0 + x, metas[x][4], parts, warp, 8, r);
+    __syncthreads();
+    if (lane == 0) {
+      ms[warp] = j.m;
+      ls[warp] = j.l;
+    }
+    os[warp][lane] = j.o;
+    __syncthreads();
+    if (warp != 0) continue;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, ms[i]);
+    Joined all{top, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = ms[i] == -INFINITY ? 0.f : fast_exp2((ms[i] - top) * p.scale_log2);
+      const float4 o = os[i][lane];
+      if (f == 0.f) continue;
+      all.l = fmaf(ls[i], f, all.l);
+      all.o.x = fmaf(o.x, f, all.o.x);
+      all.o.y = fmaf(o.y, f, all.o.y);
+      all.o.z = fmaf(o.z, f, all.o.z);
+      all.o.w = fmaf(o.w, f, all.o.w);
+    }
+    store(metas[x], all);
   }
 }
 
