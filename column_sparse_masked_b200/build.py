@@ -8,6 +8,10 @@ the static CUDA runtime (the library loads on hosts without a GPU driver).
 ``build(checks=True)`` compiles the same sources with -DFLASHMASK_CHECKS=1
 (objects under csrc/_build_checks/) into libflashmask_checks.so: the range
 checks of mask values and scheduler indices that report FLASHMASK_ERR_BOUNDS.
+
+``build_binding()`` compiles csrc/binding/paged_binding.cpp (host code, g++,
+against torch's headers) into _paged_binding.so, the marshalling of the
+paged-cache calls; ``build()`` brings it up to date as well.
 """
 from __future__ import annotations
 
@@ -16,6 +20,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -23,6 +28,8 @@ BUILD = os.path.join(CSRC, "_build")
 LIB = os.path.join(HERE, "libflashmask.so")
 BUILD_CHECKS = os.path.join(CSRC, "_build_checks")
 LIB_CHECKS = os.path.join(HERE, "libflashmask_checks.so")
+BINDING_SRC = os.path.join(CSRC, "binding", "paged_binding.cpp")
+BINDING = os.path.join(HERE, "_paged_binding.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]
@@ -36,6 +43,31 @@ def _nvcc() -> str:
 def _deps() -> list:
     return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         [os.path.join(os.path.dirname(HERE), "include", "flashmask.h")]
+
+
+def build_binding(force: bool = False) -> str:
+    """Compiles (if stale) and returns the path of _paged_binding.so."""
+    header = os.path.join(os.path.dirname(HERE), "include", "flashmask.h")
+    newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(header))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                                os.path.join(cuda, "include"), sysconfig.get_paths()["include"])),
+           BINDING_SRC, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"g++ failed: {' '.join(cmd)}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False, checks: bool = False) -> str:
@@ -75,6 +107,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, lib)
+    build_binding(force)
     return lib
 
 

@@ -19,36 +19,41 @@ tokens concerned left out.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import Optional, Tuple
 
 import torch
 
-from ._binding import _check, load_library
+from ._binding import FlashMaskError, lib_path, load_library
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
-_P, _LL, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+_calls = None
 
 
-class _Pages(ctypes.Structure):
-    _fields_ = [("k", _P), ("v", _P), ("k_scales", _P), ("v_scales", _P), ("table", _P), ("table_stride", _LL)] + \
-        [(n, _I) for n in ("B", "table_width", "num_pages", "page_size", "Hkv", "d", "bits")]
+def _load():
+    """The compiled marshalling of these calls (_paged_binding.so), bound to the library in use."""
+    global _calls
+    load_library()
+    try:
+        from . import _paged_binding
+    except ImportError as e:
+        raise RuntimeError("_paged_binding.so is missing: build it with `python column_sparse_masked_b200/build.py`") from e
+    _paged_binding.bind(lib_path())
+    _calls = _paged_binding
+    return _calls
 
 
-class _Append(ctypes.Structure):
-    _fields_ = [("q", _P), ("k", _P), ("v", _P), ("q_strides", _LL * 3), ("k_strides", _LL * 3),
-                ("v_strides", _LL * 3), ("q_out", _P), ("start", _P), ("counts", _P), ("positions", _P), ("cos", _P),
-                ("sin", _P), ("N", _I), ("Hq", _I), ("rot", _I), ("table_len", _I), ("interleaved", _I)]
+def _fail(code, where: str, explain, *args):
+    """Raises for a call that did not run: the C ABI's error, or what is wrong with its arguments."""
+    if code is not NotImplemented:
+        raise FlashMaskError(code, where)
+    explain(*args)
+    raise ValueError(f"{where}: arguments are not of the documented kind")
 
 
-class _Rows(ctypes.Structure):
-    _fields_ = [("q", _P), ("q_strides", _LL * 3), ("lens", _P), ("start", _P), ("lts", _P), ("lte", _P),
-                ("uts", _P), ("ute", _P), ("Nq", _I), ("Hq", _I), ("Hm", _I), ("Nm", _I), ("causal", _I),
-                ("scale", ctypes.c_float), ("o", _P), ("lse", _P)]
-
-
+# What the compiled marshalling checks, one by one, to name what it refused: types, dtypes and shapes whatever the
+# device, then the device.
 def _is(name: str, t, dtype, shape) -> None:
-    """Type, dtype and shape (None: any size) of one argument; the kernels trust these sizes."""
+    """Type, dtype and shape (None: any size) of one argument."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
@@ -70,34 +75,25 @@ def _placed(dev, named) -> None:
             raise ValueError(f"{n} must be contiguous")
 
 
-def _strides(name: str, t: torch.Tensor):
-    """{batch, token, head} strides of rows [B, N, H, d]; any, as long as 16-byte loads stay aligned."""
-    s = t.stride()
-    if s[3] != 1:
+def _strides(name: str, t: torch.Tensor) -> None:
+    """Rows [B, N, heads, d]: any strides, as long as 16-byte loads stay aligned."""
+    if t.stride(3) != 1:
         raise ValueError(f"{name} must have unit stride over its last dimension")
-    sh = t.shape
-    r = (s[0] if sh[0] > 1 else 0, s[1] if sh[1] > 1 else 0, s[2] if sh[2] > 1 else 0)
-    if (r[0] | r[1] | r[2]) & 7 or t.data_ptr() & 15:
+    if any(t.shape[i] > 1 and t.stride(i) % 8 for i in range(3)) or t.data_ptr() % 16:
         raise ValueError(f"{name}: strides must be multiples of 8 elements and the data 16-byte aligned")
-    return r
-
-
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
 
 
 def _pages(k_pages, v_pages, k_scales, v_scales, block_table, B=None, d=None, Hkv=None, Hq=None):
-    """Checks the cache and its table, against the caller's sizes where given; returns the C structure
-    and the sizes it holds."""
+    """The cache and its table, against the caller's sizes where given; returns its sizes and device."""
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("k_pages must be a 4-D tensor [P, Hkv, page_size, d]")
     P, H, page, last = k_pages.shape
     if k_pages.dtype is _U8:
-        bits, width = 4, 2 * last
+        width = 2 * last
         _is("k_scales", k_scales, _BF16, (P, H, page, 2))
         _is("v_scales", v_scales, _BF16, (P, H, page, 2))
     else:
-        bits, width = 16, last
+        width = last
         _is("k_pages", k_pages, _BF16, (P, H, page, last))
         if k_scales is not None or v_scales is not None:
             raise ValueError("k_scales and v_scales belong to 4-bit pages (uint8)")
@@ -121,20 +117,87 @@ def _pages(k_pages, v_pages, k_scales, v_scales, block_table, B=None, d=None, Hk
     _placed(dev, (("k_pages", k_pages), ("v_pages", v_pages), ("k_scales", k_scales), ("v_scales", v_scales)))
     if block_table.device != dev:
         raise ValueError(f"block_table is on {block_table.device}, expected {dev}")
-    c = _Pages(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), block_table.data_ptr(),
-               block_table.stride(0) if B > 1 else 0, B, M, P, page, H, width, bits)
-    return c, B, H, width, dev
+    return B, H, width, dev
 
 
-def _call(name: str, dev, *args) -> None:
-    """Runs one entry point on the current stream of `dev`, with that device current."""
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(rc, name)
+def _explain_append(k, v, k_pages, v_pages, block_table, start, counts, q, cos, sin, positions, k_scales, v_scales, q_out):
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a 4-D tensor [B, N, Hkv, d]")
+    B, N, Hkv, d = k.shape
+    _is("k", k, _BF16, (B, N, Hkv, d))
+    _is("v", v, _BF16, (B, N, Hkv, d))
+    _is("start", start, _I32, (B,))
+    if q is not None:
+        _is("q", q, _BF16, (B, N, None, d))
+        if q_out is not None:
+            _is("q_out", q_out, _BF16, (B, N, q.shape[2], d))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if counts is not None:
+        _is("counts", counts, _I32, (B,))
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin must be given together")
+    if cos is not None:
+        _is("cos", cos, _F32, (None, None))
+        _is("sin", sin, _F32, cos.shape)
+    if positions is not None:
+        if cos is None:
+            raise ValueError("positions without cos and sin")
+        _is("positions", positions, _I32, (B, N))
+    for n, t in (("k", k), ("v", v), ("q", q)):
+        if t is not None:
+            _strides(n, t)
+    _, _, _, dev = _pages(k_pages, v_pages, k_scales, v_scales, block_table, B, d, Hkv)
+    for n, t in (("k", k), ("v", v), ("q", q)):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, expected {dev}")
+    _placed(dev, (("start", start), ("counts", counts), ("cos", cos), ("sin", sin), ("positions", positions),
+                  ("q_out", q_out)))
+
+
+def _explain_attention(q, k_pages, v_pages, block_table, lens, lts, lte, uts, ute, start, k_scales, v_scales, o, lse,
+                       workspace):
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a 4-D tensor [B, Nq, Hq, d]")
+    B, Nq, Hq, d = q.shape
+    _is("q", q, _BF16, (B, Nq, Hq, d))
+    _is("lens", lens, _I32, (B,))
+    if start is not None:
+        _is("start", start, _I32, (B,))
+    vecs = (("lts", lts), ("lte", lte), ("uts", uts), ("ute", ute))
+    ref = next((x for _, x in vecs if x is not None), None)
+    if ref is not None:
+        if not isinstance(ref, torch.Tensor) or ref.dim() != 3:
+            raise ValueError("mask vectors must be 3-D tensors [B, Hm, Nm]")
+        for n, x in vecs:
+            if x is not None:
+                _is(n, x, _I32, (B, ref.shape[1], ref.shape[2]))
+        if (lts is None) != (lte is None) or (uts is None) != (ute is None):
+            raise ValueError("lts and lte, and uts and ute, must be given together")
+        if ref.shape[1] not in (1, Hq):
+            raise ValueError(f"mask vectors have {ref.shape[1]} heads, expected 1 or {Hq}")
+    _strides("q", q)
+    if o is not None or lse is not None:
+        _is("o", o, _BF16, (B, Nq, Hq, d))
+        _is("lse", lse, _F32, (B, Hq, Nq))
+    _, _, _, dev = _pages(k_pages, v_pages, k_scales, v_scales, block_table, B, d, Hq=Hq)
+    if q.device != dev:
+        raise ValueError(f"q is on {q.device}, expected {dev}")
+    _placed(dev, (("lens", lens), ("start", start), *vecs, ("o", o), ("lse", lse), ("workspace", workspace)))
+
+
+def _explain_gather(k_pages, v_pages, block_table, lens, N, k_scales, v_scales, k, v):
+    _is("lens", lens, _I32, (None,))
+    if not isinstance(N, int):
+        raise TypeError("N must be an integer")
+    if N < 0:
+        raise ValueError("N must not be negative")
+    B, Hkv, d, dev = _pages(k_pages, v_pages, k_scales, v_scales, block_table)
+    _is("lens", lens, _I32, (B,))
+    if k is not None or v is not None:
+        _is("k", k, _BF16, (B, N, Hkv, d))
+        _is("v", v, _BF16, (B, N, Hkv, d))
+    _placed(dev, (("lens", lens), ("k", k), ("v", v)))
 
 
 def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -152,70 +215,12 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     ``positions`` ``[B, N]`` int32, or start + i.  Pairs are values (i, i + rot/2), or neighbours with
     ``interleaved``.  Returns the rotated q (padding rows 0; written to ``q_out`` if given, which may be a
     contiguous q itself), or None without q."""
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("k must be a 4-D tensor [B, N, Hkv, d]")
-    B, N, Hkv, d = k.shape
-    _is("k", k, _BF16, (B, N, Hkv, d))
-    _is("v", v, _BF16, (B, N, Hkv, d))
-    _is("start", start, _I32, (B,))
-    Hq = 0
-    if q is not None:
-        _is("q", q, _BF16, (B, N, None, d))
-        Hq = q.shape[2]
-        if q_out is not None:
-            _is("q_out", q_out, _BF16, (B, N, Hq, d))
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if counts is not None:
-        _is("counts", counts, _I32, (B,))
-    rot = n_pos = 0
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin must be given together")
-    if cos is not None:
-        _is("cos", cos, _F32, (None, None))
-        _is("sin", sin, _F32, cos.shape)
-        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
-    if positions is not None:
-        if cos is None:
-            raise ValueError("positions without cos and sin")
-        _is("positions", positions, _I32, (B, N))
-    ks, vs = _strides("k", k), _strides("v", v)
-    qs = (0, 0, 0) if q is None else _strides("q", q)
-    pages, _, _, _, dev = _pages(k_pages, v_pages, k_scales, v_scales, block_table, B, d, Hkv)
-    for n, t in (("k", k), ("v", v), ("q", q)):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, expected {dev}")
-    _placed(dev, (("start", start), ("counts", counts), ("cos", cos), ("sin", sin), ("positions", positions),
-                  ("q_out", q_out)))
-    if q is not None and q_out is None:
-        q_out = torch.empty((B, N, Hq, d), dtype=_BF16, device=dev)
-    c = _Append(_ptr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(q_out), start.data_ptr(), _ptr(counts),
-                _ptr(positions), _ptr(cos), _ptr(sin), N, Hq, rot, n_pos, 1 if interleaved else 0)
-    _call("flashmask_paged_append", dev, ctypes.byref(pages), ctypes.byref(c))
-    return q_out
-
-
-def _rows(q, lens, start, lts, lte, uts, ute):
-    B, Hq = q.shape[0], q.shape[2]
-    _is("q", q, _BF16, (B, None, Hq, None))
-    _is("lens", lens, _I32, (B,))
-    if start is not None:
-        _is("start", start, _I32, (B,))
-    Hm, Nm = 1, 0
-    vecs = (("lts", lts), ("lte", lte), ("uts", uts), ("ute", ute))
-    ref = next((x for _, x in vecs if x is not None), None)
-    if ref is not None:
-        if not isinstance(ref, torch.Tensor) or ref.dim() != 3:
-            raise ValueError("mask vectors must be 3-D tensors [B, Hm, Nm]")
-        Hm, Nm = ref.shape[1], ref.shape[2]
-        for n, x in vecs:
-            if x is not None:
-                _is(n, x, _I32, (B, Hm, Nm))
-        if (lts is None) != (lte is None) or (uts is None) != (ute is None):
-            raise ValueError("lts and lte, and uts and ute, must be given together")
-        if Hm not in (1, Hq):
-            raise ValueError(f"mask vectors have {Hm} heads, expected 1 or {Hq}")
-    return Hm, Nm, vecs
+    r = (_calls or _load()).append(k, v, k_pages, v_pages, block_table, start, counts, q, cos, sin, positions, interleaved,
+                                   k_scales, v_scales, q_out)
+    if r is None or r.__class__ is torch.Tensor:
+        return r
+    _fail(r, "flashmask_paged_append", _explain_append, k, v, k_pages, v_pages, block_table, start, counts, q, cos, sin,
+          positions, k_scales, v_scales, q_out)
 
 
 def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
@@ -231,30 +236,13 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     tokens) and sees key j iff j <= p (unless ``causal`` is False) and neither LTS[j] <= p < LTE[j] nor
     UTS[j] <= p < UTE[j], with mask vectors ``[B, Hm, Nm]`` as in ``fwd`` (keys from Nm on: no
     interval).  A row that sees nothing gives 0 and -inf; what unseen keys hold has no influence."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a 4-D tensor [B, Nq, Hq, d]")
-    B, Nq, Hq, d = q.shape
-    Hm, Nm, vecs = _rows(q, lens, start, lts, lte, uts, ute)
-    qs = _strides("q", q)
-    if out is not None:
-        o, lse = out
-        _is("o", o, _BF16, (B, Nq, Hq, d))
-        _is("lse", lse, _F32, (B, Hq, Nq))
-    pages, _, _, _, dev = _pages(k_pages, v_pages, k_scales, v_scales, block_table, B, d, Hq=Hq)
-    if q.device != dev:
-        raise ValueError(f"q is on {q.device}, expected {dev}")
-    if out is None:
-        o = torch.empty((B, Nq, Hq, d), dtype=_BF16, device=dev)
-        lse = torch.empty((B, Hq, Nq), dtype=_F32, device=dev)
-    _placed(dev, (("lens", lens), ("start", start), *vecs, ("o", o), ("lse", lse), ("workspace", workspace)))
-    c = _Rows(q.data_ptr(), qs, lens.data_ptr(), _ptr(start), _ptr(lts), _ptr(lte), _ptr(uts),
-              _ptr(ute), Nq, Hq, Hm, Nm, 1 if causal else 0, scale or 0.0, o.data_ptr(), lse.data_ptr())
-    pp, cp = ctypes.byref(pages), ctypes.byref(c)
-    if workspace is None:
-        need = load_library().flashmask_paged_attention_workspace_size(pp, cp)
-        workspace = torch.empty(max(need, 256), dtype=_U8, device=dev)
-    _call("flashmask_paged_attention", dev, pp, cp, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    return o, lse
+    o, lse = out or (None, None)
+    r = (_calls or _load()).attention(q, k_pages, v_pages, block_table, lens, lts, lte, uts, ute, scale, start, causal,
+                                      k_scales, v_scales, o, lse, workspace)
+    if r.__class__ is tuple:
+        return r
+    _fail(r, "flashmask_paged_attention", _explain_attention, q, k_pages, v_pages, block_table, lens, lts, lte, uts, ute,
+          start, k_scales, v_scales, o, lse, workspace)
 
 
 def paged_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
@@ -262,18 +250,8 @@ def paged_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torc
                  out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
     """The first N positions of each sequence as dense (k, v) ``[B, N, Hkv, d]`` bf16, as ``fwd`` and ``bwd``
     take them: positions from ``lens[b]`` on are 0; 4-bit pages give the values their codes stand for."""
-    _is("lens", lens, _I32, (None,))
-    pages, B, Hkv, d, dev = _pages(k_pages, v_pages, k_scales, v_scales, block_table)
-    _is("lens", lens, _I32, (B,))
-    if N < 0:
-        raise ValueError("N must not be negative")
-    if out is not None:
-        k, v = out
-        _is("k", k, _BF16, (B, N, Hkv, d))
-        _is("v", v, _BF16, (B, N, Hkv, d))
-    else:
-        k = torch.empty((B, N, Hkv, d), dtype=_BF16, device=dev)
-        v = torch.empty((B, N, Hkv, d), dtype=_BF16, device=dev)
-    _placed(dev, (("lens", lens), ("k", k), ("v", v)))
-    _call("flashmask_paged_gather", dev, ctypes.byref(pages), lens.data_ptr(), N, k.data_ptr(), v.data_ptr())
-    return k, v
+    k, v = out or (None, None)
+    r = (_calls or _load()).gather(k_pages, v_pages, block_table, lens, N, k_scales, v_scales, k, v)
+    if r.__class__ is tuple:
+        return r
+    _fail(r, "flashmask_paged_gather", _explain_gather, k_pages, v_pages, block_table, lens, N, k_scales, v_scales, k, v)

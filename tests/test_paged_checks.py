@@ -6,7 +6,26 @@ import pytest
 import torch
 
 import column_sparse_masked_b200 as fm
-from column_sparse_masked_b200.paged import _Append, _Pages, _Rows
+
+_P, _LL, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+
+
+class _Pages(ctypes.Structure):  # flashmask_pages
+    _fields_ = [("k", _P), ("v", _P), ("k_scales", _P), ("v_scales", _P), ("table", _P), ("table_stride", _LL)] + \
+        [(n, _I) for n in ("B", "table_width", "num_pages", "page_size", "Hkv", "d", "bits")]
+
+
+class _Append(ctypes.Structure):  # flashmask_append
+    _fields_ = [("q", _P), ("k", _P), ("v", _P), ("q_strides", _LL * 3), ("k_strides", _LL * 3),
+                ("v_strides", _LL * 3), ("q_out", _P), ("start", _P), ("counts", _P), ("positions", _P), ("cos", _P),
+                ("sin", _P), ("N", _I), ("Hq", _I), ("rot", _I), ("table_len", _I), ("interleaved", _I)]
+
+
+class _Rows(ctypes.Structure):  # flashmask_paged_rows
+    _fields_ = [("q", _P), ("q_strides", _LL * 3), ("lens", _P), ("start", _P), ("lts", _P), ("lte", _P),
+                ("uts", _P), ("ute", _P), ("Nq", _I), ("Hq", _I), ("Hm", _I), ("Nm", _I), ("causal", _I),
+                ("scale", ctypes.c_float), ("o", _P), ("lse", _P)]
+
 
 B, N, HQ, HKV, D, P, PAGE, M = 2, 3, 4, 2, 64, 5, 16, 4
 BF = torch.bfloat16
