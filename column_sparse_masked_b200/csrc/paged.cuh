@@ -39,6 +39,20 @@ struct GatherParams {
   __nv_bfloat16 *k, *v;
 };
 
+// Division of numbers below 2^31 by a constant of the call: x / d = (x * m) >> 32 >> s with m = ceil(2^(32 + s) / d),
+// exact for x < 2^31 when 2^s < d <= 2^(s+1) (the error x (m d - 2^(32+s)) / (d 2^(32+s)) stays below 1 / d).
+struct FastDiv {
+  uint32_t m, s;
+  __device__ __forceinline__ int operator()(int x) const { return m ? (int)(__umulhi((uint32_t)x, m) >> s) : x; }
+};
+inline FastDiv fast_div(int d) {
+  FastDiv f{0, 0};
+  if (d <= 1) return f;
+  while ((2ull << f.s) < (uint64_t)d) ++f.s;
+  f.m = (uint32_t)(((1ull << (32 + f.s)) + d - 1) / d);
+  return f;
+}
+
 // How the work is divided: equal runs of tiles per warp (items may be cut), whole items per warp, or one
 // CTA per item.
 enum PagedMode { kPagedSplit = 0, kPagedWhole = 1, kPagedCoop = 2 };
@@ -61,6 +75,8 @@ struct PagedAttnParams {
   float* lse;
   // work: groups (a sequence, or a sequence and KV head with per-head masks) of `mult` items of `rows` rows
   int per_head, n_groups, mult, n_rb, rows, tile_keys;
+  FastDiv div_g, div_hkv, div_rb, div_mult;  // by G, Hkv, n_rb, mult
+  uint32_t q_bytes, table_bytes;  // to prefetch (0: not in one piece)
   int mode;                 // kPaged*: how the work is divided
   // plan (with mask vectors): visible tiles of each group, row-visibility words of each key
   const int* counts;        // [n_groups]
@@ -87,7 +103,7 @@ struct PlanOut {
 
 constexpr int kPagedMaxCtas = 160;
 
-__device__ __forceinline__ void record_bounds(int* status) { atomicCAS(status, 0, kDevErrBounds); }
+static __device__ __noinline__ void record_bounds(int* status) { atomicCAS(status, 0, kDevErrBounds); }
 
 // Page of position j of sequence b; -1 (recorded) for an entry out of range.
 // j must lie in [0, table_width * page_size).

@@ -238,6 +238,19 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
   p.n_rb = L.n_rb;
   p.rows = L.rows;
   p.tile_keys = L.tile_keys;
+  p.div_g = fast_div(p.G);
+  p.div_hkv = fast_div(pages->Hkv);
+  p.div_rb = fast_div(L.n_rb);
+  p.div_mult = fast_div(L.mult);
+  {
+    const int64_t row = (int64_t)r.Hq * pages->d, batch = row * r.Nq, all = batch * pages->B * 2;
+    const bool dense = (r.Hq == 1 || r.q_strides[2] == pages->d) && (r.Nq == 1 || r.q_strides[1] == row) &&
+                       (pages->B == 1 || r.q_strides[0] == batch);
+    p.q_bytes = dense && all < (1 << 20) ? (uint32_t)all : 0;
+    const int64_t table = (int64_t)pages->B * pages->table_width * 4;
+    const bool whole = pages->B == 1 || pages->table_stride == pages->table_width;
+    p.table_bytes = whole && table < (1 << 20) ? (uint32_t)table : 0;
+  }
   p.mode = L.mode;
   p.part = reinterpret_cast<float*>(ws + L.part);
   p.stat = reinterpret_cast<float2*>(ws + L.stat);

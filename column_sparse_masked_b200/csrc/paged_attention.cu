@@ -51,22 +51,23 @@ constexpr int kMinUnits = 4;  // units that a run holds at least (kItemCost of t
 // ---------------------------------------------------------------------------
 // work: groups of items with the same number of tiles, and a CTA's run of units
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int group_batch(const PagedAttnParams& p, int g) { return p.per_head ? g / p.pg.Hkv : g; }
+__device__ __forceinline__ int group_batch(const PagedAttnParams& p, int g) { return p.per_head ? p.div_hkv(g) : g; }
 
 // A sequence as the kernels use it: cached keys, and its first row's position.
+// Positions beyond +-2^30 see what those see (keys are fewer), so sums with row
+// numbers stay in 32 bits.
 struct Seq {
   int len, first;
 };
 __device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
   Seq q;
   q.len = checked_len(p.pg, p.lens, b);
-  q.first = p.start ? p.start[b] : q.len - p.Nq;
+  q.first = p.start ? min(max(p.start[b], -(1 << 30)), 1 << 30) : q.len - p.Nq;
   return q;
 }
 // Keys that the sequence's rows can see at all.
 __device__ __forceinline__ int key_bound(const PagedAttnParams& p, const Seq& q) {
-  const int64_t hi = p.causal ? min((int64_t)q.len, (int64_t)q.first + p.Nq) : (int64_t)q.len;
-  return hi > 0 ? (int)hi : 0;
+  return p.causal ? max(min(q.len, q.first + p.Nq), 0) : q.len;
 }
 
 __device__ __forceinline__ int load_tiles(const PagedAttnParams& p, int g) {
@@ -140,9 +141,9 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const PagedAttnParams& p, int g, int in, int rows_per_item) {
   Item it;
-  const int kv = p.n_rb == 1 ? in : in / p.n_rb;
+  const int kv = p.div_rb(in);
   it.b = group_batch(p, g);
-  it.kvh = p.per_head ? g % p.pg.Hkv : kv;
+  it.kvh = p.per_head ? g - it.b * p.pg.Hkv : kv;
   it.row0 = (in - kv * p.n_rb) * rows_per_item;
   return it;
 }
@@ -319,8 +320,7 @@ struct Issuer {
       } else {
         j0 = t * KT;
         // keys that every row of the item sees
-        const int64_t all = p.causal ? min((int64_t)seq.len, (int64_t)seq.first + it.row0 / p.G + 1) : (int64_t)seq.len;
-        masked = (int64_t)j0 + KT > all;
+        masked = j0 + KT > (p.causal ? min(seq.len, seq.first + p.div_g(it.row0) + 1) : seq.len);
       }
 #pragma unroll
       for (int i = 0; i < C::kBoxes; ++i) {
@@ -421,7 +421,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
   float qsum[2 * NT];
   uint2* qw = sm.q + warp * (C::kQBytes / 8);
   auto row_ptr = [&](const Item& it, int r) {
-    const int row = it.row0 + r, i = p.Nq == 1 ? 0 : row / p.G;
+    const int row = it.row0 + r, i = p.div_g(row);
     return p.q + it.b * p.qs[0] + i * p.qs[1] + (it.kvh * p.G + row - i * p.G) * p.qs[2];
   };
   auto load_q = [&](const Item& it) {
@@ -646,19 +646,19 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const int row = it.row0 + nt * 8 + 2 * q4 + e, i = row / p.G;
+                  const int row = it.row0 + nt * 8 + 2 * q4 + e, i = p.div_g(row);
                   bool see;
                   if (p.words_shared) {
                     see = (w >> (i & 31)) & 1u;
                   } else if (p.words) {
                     see = false;
                     if (i < p.Nq && there) {
-                      const int hm = p.Hm == 1 ? 0 : it.kvh * p.G + row % p.G;
+                      const int hm = p.Hm == 1 ? 0 : it.kvh * p.G + row - i * p.G;
                       const int64_t at = ((int64_t)(it.b * p.Hm + hm) * p.n_words + (i >> 5)) * p.words_stride + j;
                       see = (p.words[at] >> (i & 31)) & 1u;
                     }
                   } else {
-                    see = j < seq.len && (!p.causal || j <= (int64_t)seq.first + i);
+                    see = j < seq.len && (!p.causal || j <= seq.first + i);
                   }
                   if (!(see && there)) {
                     hid |= 1u << ((m2 * 2 + hf) * 2 * NT + nt * 2 + e);
@@ -884,7 +884,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
           o.z += v.z;
           o.w += v.w;
         }
-        const int row = it.row0 + r, i = row / p.G, h = it.kvh * p.G + row % p.G;
+        const int row = it.row0 + r, i = p.div_g(row), h = it.kvh * p.G + row - i * p.G;
         const float inv = top == -INFINITY ? 0.f : 1.f / L;
         *reinterpret_cast<uint2*>(p.o + (((int64_t)it.b * p.Nq + i) * p.Hq + h) * D + 4 * d4) =
             make_uint2(pack_bf16x2((o.x + cc) * inv, (o.y + cc) * inv), pack_bf16x2((o.z + cc) * inv, (o.w + cc) * inv));
@@ -897,9 +897,9 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
 #pragma unroll
       for (int x = 0; x < 2 * NT; ++x) {
         const float inv = mx[x] == -INFINITY ? 0.f : 1.f / sum[x];
-        const int r = (x >> 1) * 8 + 2 * q4 + (x & 1), row = it.row0 + r, i = row / p.G;
+        const int r = (x >> 1) * 8 + 2 * q4 + (x & 1), row = it.row0 + r, i = p.div_g(row);
         if (g8 == 0 && r < R)
-          p.lse[((int64_t)it.b * p.Hq + it.kvh * p.G + row % p.G) * p.Nq + i] =
+          p.lse[((int64_t)it.b * p.Hq + it.kvh * p.G + row - i * p.G) * p.Nq + i] =
               mx[x] == -INFINITY ? -INFINITY : fmaf(mx[x], p.scale_log2, log2f(sum[x])) * kLn2;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -910,8 +910,8 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (BITS == 16) {  // 8 x 8 blocks turned, so that a lane has neighbouring values of one row
-          const int r = nt * 8 + g8, row = it.row0 + r, i = row / p.G;
-          __nv_bfloat16* dst = p.o + (((int64_t)it.b * p.Nq + i) * p.Hq + it.kvh * p.G + row % p.G) * D + 2 * q4;
+          const int r = nt * 8 + g8, row = it.row0 + r, i = p.div_g(row);
+          __nv_bfloat16* dst = p.o + (((int64_t)it.b * p.Nq + i) * p.Hq + it.kvh * p.G + row - i * p.G) * D + 2 * q4;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -922,9 +922,9 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
         } else {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int r = nt * 8 + 2 * q4 + e, row = it.row0 + r, i = row / p.G;
+            const int r = nt * 8 + 2 * q4 + e, row = it.row0 + r, i = p.div_g(row);
             if (r >= R) continue;
-            __nv_bfloat16* dst = p.o + (((int64_t)it.b * p.Nq + i) * p.Hq + it.kvh * p.G + row % p.G) * D + g8 * (D / 8);
+            __nv_bfloat16* dst = p.o + (((int64_t)it.b * p.Nq + i) * p.Hq + it.kvh * p.G + row - i * p.G) * D + g8 * (D / 8);
 #pragma unroll
             for (int mt = 0; mt < MT; mt += 4)
               *reinterpret_cast<uint4*>(dst + 2 * mt) =
@@ -1012,17 +1012,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
   wc.smem_base = smem_addr(raw);
   wc.kernel = 5;
   // Rows of Q and the page table towards the L2: a batch's keys have evicted them since the last call, and
-  // one run's chain of lengths, pages, rows and tiles would pay for each in turn.  (No value is read.)
+  // a run's chain of lengths, pages, rows and tiles would wait for each in turn.  (No value is read.)
   {
-    const int n = p.pg.B * p.Nq * p.Hq, at = blockIdx.x * C::kThreads + tid, all = gridDim.x * C::kThreads;
-    for (int r = at; r < min(n, 2 * all); r += all) {
-      const int h = r % p.Hq, bi = r / p.Hq, b = bi / p.Nq;
-      prefetch_l2(p.q + b * p.qs[0] + (bi - b * p.Nq) * p.qs[1] + h * p.qs[2]);
-      if (D == 128) prefetch_l2(p.q + b * p.qs[0] + (bi - b * p.Nq) * p.qs[1] + h * p.qs[2] + 64);
-    }
-    const int lines = (p.pg.table_width + 31) / 32;
-    for (int r = at; r < min(p.pg.B * lines, 2 * all); r += all)
-      prefetch_l2(p.pg.table + (r / lines) * p.pg.table_stride + (r % lines) * 32);
+    const uint32_t at = (blockIdx.x * C::kThreads + tid) * 128;
+    if (at < p.q_bytes) prefetch_l2(reinterpret_cast<const char*>(p.q) + at);
+    if (at < p.table_bytes) prefetch_l2(reinterpret_cast<const char*>(p.pg.table) + at);
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -1051,7 +1045,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
       wk.left = q + (worker < rem ? 1 : 0);
       works = wk.left > 0;
     }
-    wk.g = works ? first / p.mult : 0;
+    wk.g = works ? p.div_mult(first) : 0;
     wk.in = first - wk.g * p.mult;
     wk.T = sq.tiles(p, wk.g);
     wk.pos = wk.base = 0;
@@ -1181,7 +1175,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
     metas[tid / kMetaInts][tid % kMetaInts] = v0 + tid / kMetaInts < workers ? p.meta[v0 * kMetaInts + tid] : -1;
   __syncthreads();
   auto store = [&](const int* meta, const Joined& j) {
-    const int row = meta[2] + r, i = row / p.G, h = meta[1] * p.G + row - i * p.G, d4 = lane % (D / 4);
+    const int row = meta[2] + r, i = p.div_g(row), h = meta[1] * p.G + row - i * p.G, d4 = lane % (D / 4);
     const float inv = j.m == -INFINITY ? 0.f : 1.f / j.l;
     if (lane >= D / 4) return;
     *reinterpret_cast<uint2*>(p.o + (((int64_t)meta[0] * p.Nq + i) * p.Hq + h) * D + 4 * d4) =
@@ -1250,6 +1244,7 @@ __global__ void __launch_bounds__(256) paged_plan_kernel(const __grid_constant__
   const int hm0 = p.per_head ? (g % p.pg.Hkv) * p.G : 0, nh = p.per_head ? p.G : 1;
   const Seq seq = load_seq(p, b);
   const int hi = key_bound(p, seq);
+  const int64_t first = p.start ? (int64_t)p.start[b] : (int64_t)seq.first;  // as given: masks are applied literally
   if (t * KT >= hi) return;
   bool any = false, all = true;
   for (int h = 0; h < nh; ++h) {
@@ -1275,7 +1270,7 @@ __global__ void __launch_bounds__(256) paged_plan_kernel(const __grid_constant__
     for (int y = 0; y < KT / 32; ++y) {
       const int j = t * KT + y * 32 + lane;
       for (int w = 0; w < p.n_words; ++w) {
-        const int64_t p0 = (int64_t)seq.first + 32 * w;
+        const int64_t p0 = first + 32 * w;
         const uint32_t rows = bit_range(0, min(32, p.Nq - 32 * w));
         uint32_t see = 0;
         if (j < hi) {
