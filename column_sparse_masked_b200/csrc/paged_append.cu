@@ -70,18 +70,25 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float (&c)[8], cons
   }
 }
 
-// The code of x in a row with minimum lo: the integer nearest to (x - lo) /
-// scale, ties to even.  The quotient only proposes; the decision at k + 1/2 is
-// the sign of (x - lo) - (k + 1/2) scale, which fp32 gives without error (the
-// product has 13 bits, and the difference x - lo comes with its rounding
-// error), so that no rounding moves a value across the middle of two codes.
-__device__ __forceinline__ uint32_t code_of(float x, float lo, float scale, float inv) {
-  const float diff = x - lo, z = diff - x;
-  const float err = (x - (diff - z)) + (-lo - z);
-  const float k = fminf(floorf(diff * inv), 15.f);
-  const float r = fmaf(-scale, k + 0.5f, diff) + err;
-  const uint32_t ki = (uint32_t)k;
-  return min(ki + ((r > 0.f || (r == 0.f && (ki & 1u))) ? 1u : 0u), 15u);
+// The code of x in a row with minimum lo, as a float: the integer nearest to
+// (x - lo) / scale, ties to even.  The quotient in fp32 only proposes; the
+// decision is |x - lo - k scale| against half the scale, which fp32 gives
+// without error (k scale has 12 bits, and the difference x - lo comes with its
+// rounding error, Knuth's sum).  Ties are common, since values and scales lie on
+// the same few binary places: one value in some 300 of normal data.
+__device__ __forceinline__ float code_of(float x, float lo, float scale, float inv, float half, float below_half) {
+  const float diff = x - lo, z = diff - x, err = (x - (diff - z)) + (-lo - z);
+  const float m = fmaf(diff, inv, 12582912.f), k = m - 12582912.f;  // to an integer, which is in m's low bits
+  const float e = fmaf(-k, scale, diff) + err;
+  const float limit = (__float_as_uint(m) & 1u) ? below_half : half;  // an odd code gives way at the middle
+  return fabsf(e) > limit ? k + copysignf(1.f, e) : k;
+}
+
+// Lower of two bf16 pairs, NaN if either is.
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // One thread takes 16 values of a row (two 16-byte chunks that hold whole
@@ -141,29 +148,30 @@ __global__ void __launch_bounds__(128) paged_append_kernel(AppendParams p, int g
     a = 8 * e;
     bo = p.rot / 2 + 8 * e;
   }
-  const int Hq = p.q ? p.Hq : 0, rows = Hq + 2 * p.pg.Hkv;
-  for (int r = g0; r < rows; r += 1 << gpt_log2) {
-    float x[16];
-    uint32_t w[8];
-    if (r < Hq) {
-      __nv_bfloat16* out = p.q_out + (token * Hq + r) * D;
+  const int Hq = p.q ? p.Hq : 0, Hkv = p.pg.Hkv, step = 1 << gpt_log2;
+  int r = g0;
+  {
+    const __nv_bfloat16* qb = p.q + b * p.qs[0] + i * p.qs[1];
+    __nv_bfloat16* ob = p.q_out + token * Hq * D;
+    for (; r < Hq; r += step) {
+      uint32_t w[8] = {};
       if (turn_ok) {
-        load_chunks(p.q + b * p.qs[0] + i * p.qs[1] + r * p.qs[2], a, bo, x);
+        float x[16];
+        load_chunks(qb + r * p.qs[2], a, bo, x);
         if (turns) rotate<false>(x, c, s, p.interleaved);
         pack_chunks(x, w);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 0u;
       }
-      store_chunks(out, a, bo, w);
-      continue;
+      store_chunks(ob + r * D, a, bo, w);
     }
-    if (!store_ok) continue;
-    const bool is_k = r < Hq + p.pg.Hkv;
-    const int h = is_k ? r - Hq : r - Hq - p.pg.Hkv;
-    const __nv_bfloat16* src =
-        is_k ? p.k + b * p.ks[0] + i * p.ks[1] + h * p.ks[2] : p.v + b * p.vs[0] + i * p.vs[1] + h * p.vs[2];
-    load_chunks(src, a, bo, x);
+  }
+  if (!store_ok) return;
+  const __nv_bfloat16 *kb = p.k + b * p.ks[0] + i * p.ks[1], *vb = p.v + b * p.vs[0] + i * p.vs[1];
+  for (r -= Hq; r < 2 * Hkv; r += step) {
+    float x[16];
+    uint32_t w[8];
+    const bool is_k = r < Hkv;
+    const int h = is_k ? r : r - Hkv;
+    load_chunks(is_k ? kb + h * p.ks[2] : vb + h * p.vs[2], a, bo, x);
     if (is_k && turns) rotate<BITS == 4>(x, c, s, p.interleaved);
     pack_chunks(x, w);
     const int64_t row = row_of(p.pg, page, h, (int)pos);
@@ -172,42 +180,75 @@ __global__ void __launch_bounds__(128) paged_append_kernel(AppendParams p, int g
       store_chunks(reinterpret_cast<__nv_bfloat16*>(dst), a, bo, w);
       continue;
     }
-    float lo = INFINITY, hi = -INFINITY;
-    bool bad = false;
+    // Minimum and negated maximum of the row, side by side in one bf16 pair (NaN stays NaN).
+    uint32_t ends;
+    {
+      uint32_t mn = w[0], mx = w[0] ^ 0x80008000u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[2 * j] = __uint_as_float(w[j] << 16);
-      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      lo = fminf(lo, fminf(x[2 * j], x[2 * j + 1]));
-      hi = fmaxf(hi, fmaxf(x[2 * j], x[2 * j + 1]));
-      bad |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+      for (int j = 1; j < 8; ++j) {
+        mn = min2(mn, w[j]);
+        mx = min2(mx, w[j] ^ 0x80008000u);
+      }
+      ends = min2(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
     }
 #pragma unroll
-    for (int o = 1; o < L; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(gmask, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(gmask, hi, o));
-    }
-    const float spread = hi - lo;
-    bad = __any_sync(gmask, bad) || spread == INFINITY;
-    const uint32_t sm = bad ? 0x7fff7fffu : pack_bf16x2(__fdiv_rn(spread, 15.f), lo);
+    for (int o = 1; o < L; o <<= 1) ends = min2(ends, __shfl_xor_sync(gmask, ends, o));
+    float lo = __uint_as_float(ends << 16);
+    const float spread = -__uint_as_float(ends & 0xffff0000u) - lo;
+    const uint32_t sm = spread < INFINITY ? pack_bf16x2(__fdiv_rn(spread, 15.f), lo) : 0x7fff7fffu;  // else NaN
     float scale = __uint_as_float(sm << 16);
     uint32_t w0 = 0u, w1 = 0u;
     if (scale > 0.f) {  // false for a row of equal values and for NaN
-      // tiny scales have no reciprocal: the row is scaled by a power of two
-      const float up = scale < 0x1p-100f ? 0x1p64f : 1.f;
-      scale *= up;
-      lo *= up;
-      const float inv = 1.f / scale;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        w0 |= code_of(x[j] * up, lo, scale, inv) << (4 * j);
-        w1 |= code_of(x[8 + j] * up, lo, scale, inv) << (4 * j);
+        x[2 * j] = __uint_as_float(w[j] << 16);
+        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
       }
+      const bool tiny = scale < 0x1p-100f;
+      if (tiny) {  // no reciprocal: the row is scaled by a power of two
+        scale *= 0x1p64f;
+        lo *= 0x1p64f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] *= 0x1p64f;
+      }
+      const float inv = 1.f / scale, half = 0.5f * scale, below_half = __uint_as_float(__float_as_uint(half) - 1u);
+      // codes are put together four at a time as a sum of code * 16^j, exact in fp32
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float k = code_of(x[j], lo, scale, inv, half, below_half);
+        if (tiny) k = fminf(k, 15.f);  // the scale of so small a spread may be rounded down by a half
+        part[j >> 2] = fmaf(k, (float)(1 << (4 * (j & 3))), part[j >> 2]);
+      }
+      w0 = (uint32_t)part[0] | (uint32_t)part[1] << 16;
+      w1 = (uint32_t)part[2] | (uint32_t)part[3] << 16;
     }
     *reinterpret_cast<uint32_t*>(dst + a / 2) = w0;
     *reinterpret_cast<uint32_t*>(dst + bo / 2) = w1;
     if (e == 0) (is_k ? p.pg.k_scales : p.pg.v_scales)[row] = sm;
   }
+}
+
+// Eight values minimum + scale * code (codes: nibbles of x, in order) as four
+// bf16 pairs.  A fused bf16 multiply-add rounds the exact value once; the
+// same comes of rounding it to fp32 and then to bf16, since the sum has at most
+// 24 bits wherever it lies near the middle of two bf16 values (a code times a
+// scale has 12, and more than 12 binary places below the minimum's last it
+// cannot reach that middle).
+__device__ __forceinline__ void values8(uint32_t x, __nv_bfloat162 scale, __nv_bfloat162 lo, uint32_t* out) {
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // codes i and i + 4
+    uint32_t y;
+    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(y) : "r"(x >> (4 * i)));  // 128 + code
+    asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(0x43004300u));
+    const __nv_bfloat162 r = __hfma2(scale, *reinterpret_cast<__nv_bfloat162*>(&y), lo);
+    v[i] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  out[0] = __byte_perm(v[0], v[1], 0x5410);
+  out[1] = __byte_perm(v[2], v[3], 0x5410);
+  out[2] = __byte_perm(v[0], v[1], 0x7632);
+  out[3] = __byte_perm(v[2], v[3], 0x7632);
 }
 
 // One thread writes 16 values of k and of v (32-byte stores, whole rows by
@@ -238,14 +279,12 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(GatherParams p, int64
         const uint2 ck = *reinterpret_cast<const uint2*>(p.pg.k + row * (D / 2) + 8 * e);
         const uint2 cv = *reinterpret_cast<const uint2*>(p.pg.v + row * (D / 2) + 8 * e);
         const uint32_t ks = p.pg.k_scales[row], vs = p.pg.v_scales[row];
-        const float k_s = __uint_as_float(ks << 16), k_m = __uint_as_float(ks & 0xffff0000u);
-        const float v_s = __uint_as_float(vs << 16), v_m = __uint_as_float(vs & 0xffff0000u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // scale * code has 12 bits: the sum is rounded to fp32 once, then to bf16
-          const uint32_t c = (i < 4 ? ck.x : ck.y) >> (8 * (i & 3)), f = (i < 4 ? cv.x : cv.y) >> (8 * (i & 3));
-          wk[i] = pack_bf16x2(fmaf(k_s, (float)(c & 15u), k_m), fmaf(k_s, (float)((c >> 4) & 15u), k_m));
-          wv[i] = pack_bf16x2(fmaf(v_s, (float)(f & 15u), v_m), fmaf(v_s, (float)((f >> 4) & 15u), v_m));
-        }
+        const __nv_bfloat162 km = *reinterpret_cast<const __nv_bfloat162*>(&ks);
+        const __nv_bfloat162 vm = *reinterpret_cast<const __nv_bfloat162*>(&vs);
+        values8(ck.x, __low2bfloat162(km), __high2bfloat162(km), wk);
+        values8(ck.y, __low2bfloat162(km), __high2bfloat162(km), wk + 4);
+        values8(cv.x, __low2bfloat162(vm), __high2bfloat162(vm), wv);
+        values8(cv.y, __low2bfloat162(vm), __high2bfloat162(vm), wv + 4);
       }
     }
   }

@@ -711,10 +711,14 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
                 sum[x] += pr;
                 w[e] = pr;
                 if (BITS == 4) {
-                  // a hidden key's scale may be anything, NaN included
-                  const bool hidden = (hid >> ((m2 * 2 + hf) * 2 * NT + x)) & 1u;
-                  w[e] = hidden ? 0.f : pr * vs[m2][hf];
-                  cor[x] = hidden ? cor[x] : fmaf(pr, vm[m2][hf], cor[x]);
+                  w[e] = pr * vs[m2][hf];
+                  if (!masked) {
+                    cor[x] = fmaf(pr, vm[m2][hf], cor[x]);
+                  } else {  // a hidden key's scale may be anything, NaN included
+                    const bool hidden = (hid >> ((m2 * 2 + hf) * 2 * NT + x)) & 1u;
+                    w[e] = hidden ? 0.f : w[e];
+                    cor[x] = hidden ? cor[x] : fmaf(pr, vm[m2][hf], cor[x]);
+                  }
                 } else {
                   s[m2][nt][2 * hf + e] = pr;
                 }
