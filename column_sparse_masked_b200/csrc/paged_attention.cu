@@ -1098,8 +1098,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
   if (COOP || p.mode == kPagedWhole) wk.cut(p);
   if (works) attend<D, BITS, NT, COOP>(p, &tk, &tv, sm, sq, wk, wc, run);
   if (COOP || p.mode == kPagedWhole) return;
-  for (int g = blockIdx.x; g < p.n_groups; g += gridDim.x)
-    if (sq.tiles(p, g) == 0) write_empty<D>(p, g, C::kThreads);
+  if constexpr (!COOP)
+    for (int g = blockIdx.x; g < p.n_groups; g += gridDim.x)
+      if (sq.tiles(p, g) == 0) write_empty<D>(p, g, C::kThreads);
 }
 
 // ---------------------------------------------------------------------------
