@@ -82,10 +82,9 @@ struct PagedAttnParams {
   const int* counts;        // [n_groups]
   const int* list;          // [n_groups, list_stride]: tile << 1 | some pair hidden
   int list_stride;
-  const uint32_t* words;    // [B, Hm, n_words, words_stride]: bit i = row 32 w + i sees the key
+  const uint32_t* words;    // [n_groups, n_words, words_stride]: bit i = row 32 w + i of the KV head sees the key
   int n_words;
   int64_t words_stride;
-  int words_shared;         // one word per key serves all rows
   // partial sums of cut items: two slots per run (worker: a warp)
   float* part;              // [2 workers, rows, d]
   float2* stat;             // [2 workers, rows]: running maximum, sum

@@ -95,7 +95,7 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
   L.n_groups = L.per_head ? pg.B * pg.Hkv : pg.B;
   L.mult = L.per_head ? L.n_rb : pg.Hkv * L.n_rb;
   L.tile_keys = paged_tile_keys(pg.d, pg.bits);
-  L.n_words = (r.Nq + 31) / 32;
+  L.n_words = (int)((R + 31) / 32);
   const int64_t cap = (int64_t)pg.table_width * pg.page_size;
   L.keys = (cap + L.tile_keys - 1) / L.tile_keys * L.tile_keys;
   size_t off = 0;
@@ -115,7 +115,7 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
   if (masked) {
     L.counts = take((size_t)L.n_groups * 4);
     L.list = take((size_t)L.n_groups * (L.keys / L.tile_keys) * 4);
-    L.words = take((size_t)pg.B * r.Hm * L.n_words * L.keys * 4);
+    L.words = take((size_t)L.n_groups * L.n_words * L.keys * 4);
     L.flags = take((size_t)L.n_groups * (L.keys / L.tile_keys));
   }
   L.bytes = off > 0 ? off : 256;
@@ -264,7 +264,6 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
     p.list_stride = (int)(L.keys / L.tile_keys);
     p.n_words = L.n_words;
     p.words_stride = L.keys;
-    p.words_shared = p.Hm == 1 && L.n_words == 1;
   }
   p.wait_limit_ns = wait_limit_ns();
   CUtensorMap tk{}, tv{};

@@ -46,7 +46,7 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kMetaInts = 8;
-constexpr int kMinUnits = 4;  // units that a run holds at least (kItemCost of them may stand for an item)
+constexpr int kMinUnits = 2;  // units that a run holds at least (kItemCost of them may stand for an item)
 
 // ---------------------------------------------------------------------------
 // work: groups of items with the same number of tiles, and a CTA's run of units
@@ -531,6 +531,13 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
 
     }
     const int stage = warp * C::kDepth + taken % C::kDepth;
+    // row-visibility words of the thread's keys, asked for before the tile is waited for
+    uint32_t seen[KT / 32 * 4];
+    if (p.words && ahead > 0 && k < wk.n && sm.hdr[stage].y) {
+      const uint32_t* w = p.words + ((int64_t)wk.g * p.n_words + (it.row0 >> 5)) * p.words_stride + sm.hdr[stage].x;
+#pragma unroll
+      for (int y = 0; y < KT / 32 * 4; ++y) seen[y] = w[(y >> 2) * 32 + (y & 3) * 8 + (BITS == 4 ? slot_key(g8) : g8)];
+    }
     if (BITS == 16 && ahead > 0 && k < wk.n) {
       if (alive) alive = mbar_wait(&sm.full[stage], (taken / C::kDepth) & 1u, wc);
       alive = __all_sync(0xffffffffu, alive);
@@ -641,25 +648,14 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
             for (int hf = 0; hf < 2; ++hf) {
               const int key = key_of(m2, hf), j = hd.x + key;
               const bool there = (hd.z >> (key >> box_shift)) & 1;
-              const uint32_t w = p.words_shared && there ? p.words[(int64_t)it.b * p.words_stride + j] : 0u;
+              const uint32_t w = sb == 0 ? seen[m2 * 2 + hf] : seen[(KT / 32 - 1) * 4 + m2 * 2 + hf];
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const int row = it.row0 + nt * 8 + 2 * q4 + e, i = p.div_g(row);
-                  bool see;
-                  if (p.words_shared) {
-                    see = (w >> (i & 31)) & 1u;
-                  } else if (p.words) {
-                    see = false;
-                    if (i < p.Nq && there) {
-                      const int hm = p.Hm == 1 ? 0 : it.kvh * p.G + row - i * p.G;
-                      const int64_t at = ((int64_t)(it.b * p.Hm + hm) * p.n_words + (i >> 5)) * p.words_stride + j;
-                      see = (p.words[at] >> (i & 31)) & 1u;
-                    }
-                  } else {
-                    see = j < seq.len && (!p.causal || j <= seq.first + i);
-                  }
+                  const int r = nt * 8 + 2 * q4 + e;
+                  const bool see = p.words ? (w >> r) & 1u
+                                           : j < seq.len && (!p.causal || j <= seq.first + p.div_g(it.row0 + r));
                   if (!(see && there)) {
                     hid |= 1u << ((m2 * 2 + hf) * 2 * NT + nt * 2 + e);
                     s[m2][nt][2 * hf + e] = -INFINITY;
@@ -1232,9 +1228,9 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
 // group that does both in one launch took 30 us for one sequence of 128K keys:
 // 8 SMs do not have enough loads in flight for 2 MB of vectors.
 // ---------------------------------------------------------------------------
-// Rows [p0, p0 + 32) with [lo, hi) cut out, as a word.
-__device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t p0) {
-  const int a = (int)min(max(lo - p0, (int64_t)0), (int64_t)32), b = (int)min(max(hi - p0, (int64_t)0), (int64_t)32);
+// The rows of [r0, r0 + 32) that lie in [lo, hi), as a word.
+__device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t r0) {
+  const int a = (int)min(max(lo - r0, (int64_t)0), (int64_t)32), b = (int)min(max(hi - r0, (int64_t)0), (int64_t)32);
   return bit_range(a, b);
 }
 
@@ -1246,47 +1242,56 @@ __global__ void __launch_bounds__(256) paged_plan_kernel(const __grid_constant__
   const int g = x / p.list_stride, t = x - g * p.list_stride;
   if (g >= p.n_groups) return;
   const int b = group_batch(p, g);
-  const int hm0 = p.per_head ? (g % p.pg.Hkv) * p.G : 0, nh = p.per_head ? p.G : 1;
+  const int hm0 = p.per_head ? (g - b * p.pg.Hkv) * p.G : 0, nh = p.per_head ? p.G : 1;
   const Seq seq = load_seq(p, b);
-  const int hi = key_bound(p, seq);
+  const int hi = key_bound(p, seq), R = p.Nq * p.G;
   const int64_t first = p.start ? (int64_t)p.start[b] : (int64_t)seq.first;  // as given: masks are applied literally
   if (t * KT >= hi) return;
+  // Rows are numbered position by position, the heads of one position together: an interval of positions is
+  // an interval of rows, of which a head has every G-th.
+  auto rows_hidden = [&](int64_t lo, int64_t end, int r0) { return rows_in((lo - first) * p.G, (end - first) * p.G, r0); };
   bool any = false, all = true;
-  for (int h = 0; h < nh; ++h) {
-    const int64_t at = ((int64_t)b * p.Hm + hm0 + h);
-    int4 v[KT / 32];
+#pragma unroll 1
+  for (int w = 0; w < p.n_words; ++w) {
+    const int r0 = 32 * w;
+    const uint32_t rows = bit_range(0, min(32, R - r0));
+    uint32_t hid[KT / 32] = {};
+    for (int h = 0; h < nh; ++h) {
+      uint32_t mine = 0xffffffffu;  // rows of the head
+      if (p.per_head) {
+        mine = 0u;
+        for (int r = h - r0 % p.G; r < 32; r += p.G)
+          if (r >= 0) mine |= 1u << r;
+      }
+      int4 v[KT / 32];
 #pragma unroll
-    for (int y = 0; y < KT / 32; ++y) {
-      const int j = t * KT + y * 32 + lane;
-      const int64_t m = at * p.Nm + j;
-      v[y] = make_int4(0, 0, 0, 0);
-      if (j < p.Nm && j < hi) {
-        if (p.lts) {
-          v[y].x = p.lts[m];
-          v[y].y = p.lte[m];
-        }
-        if (p.uts) {
-          v[y].z = p.uts[m];
-          v[y].w = p.ute[m];
+      for (int y = 0; y < KT / 32; ++y) {
+        const int j = t * KT + y * 32 + lane;
+        const int64_t m = ((int64_t)b * p.Hm + hm0 + h) * p.Nm + j;
+        v[y] = make_int4(0, 0, 0, 0);
+        if (j < p.Nm && j < hi) {
+          if (p.lts) {
+            v[y].x = p.lts[m];
+            v[y].y = p.lte[m];
+          }
+          if (p.uts) {
+            v[y].z = p.uts[m];
+            v[y].w = p.ute[m];
+          }
         }
       }
+#pragma unroll
+      for (int y = 0; y < KT / 32; ++y)
+        hid[y] |= (rows_hidden(v[y].x, v[y].y, r0) | rows_hidden(v[y].z, v[y].w, r0)) & mine;
     }
 #pragma unroll
     for (int y = 0; y < KT / 32; ++y) {
       const int j = t * KT + y * 32 + lane;
-      for (int w = 0; w < p.n_words; ++w) {
-        const int64_t p0 = first + 32 * w;
-        const uint32_t rows = bit_range(0, min(32, p.Nq - 32 * w));
-        uint32_t see = 0;
-        if (j < hi) {
-          uint32_t hid = rows_in(v[y].x, v[y].y, p0) | rows_in(v[y].z, v[y].w, p0);
-          if (p.causal) hid |= rows_in(p0, j, p0);
-          see = rows & ~hid;
-        }
-        out.words[(at * p.n_words + w) * p.words_stride + j] = see;
-        any |= see != 0;
-        all &= see == rows;
-      }
+      if (p.causal) hid[y] |= rows_hidden(first, j, r0);
+      const uint32_t see = j < hi ? rows & ~hid[y] : 0u;
+      out.words[((int64_t)g * p.n_words + w) * p.words_stride + j] = see;
+      any |= see != 0;
+      all &= see == rows;
     }
   }
   any = __any_sync(0xffffffffu, any);
