@@ -80,39 +80,39 @@ int check_paged_rows(const flashmask_pages* pg, const flashmask_paged_rows* r) {
 
 // Work split and workspace of an attention call.
 struct PagedLayout {
-  int masked, per_head, n_groups, mult, n_rb, rows, tile_keys, n_words, mode;
+  int plan, per_head, n_groups, mult, n_rb, rows, tile_keys, n_words, mode;
   int64_t keys;  // capacity of the table, in whole tiles
   size_t part, stat, meta, counts, list, words, flags, bytes;
 };
 
 PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& r) {
   PagedLayout L{};
-  const bool masked = L.masked = (r.lts || r.uts) && pg.table_width > 0;
   const int64_t R = (int64_t)r.Nq * (r.Hq / pg.Hkv);
   L.rows = R <= 8 ? 8 : R <= 16 ? 16 : 32;
   L.n_rb = (int)((R + L.rows - 1) / L.rows);
-  L.per_head = masked && r.Hm > 1;
-  L.n_groups = L.per_head ? pg.B * pg.Hkv : pg.B;
-  L.mult = L.per_head ? L.n_rb : pg.Hkv * L.n_rb;
   L.tile_keys = paged_tile_keys(pg.d, pg.bits);
   L.n_words = (int)((R + 31) / 32);
   const int64_t cap = (int64_t)pg.table_width * pg.page_size;
   L.keys = (cap + L.tile_keys - 1) / L.tile_keys * L.tile_keys;
-  size_t off = 0;
-  auto take = [&](size_t bytes) { const size_t o = off; off = ws_align(off + bytes); return o; };
   // Whole items where cutting has nothing to give, and no second kernel: one per CTA if the device takes
-  // them all at once and the table bounds them to four tiles a warp, else one after another per warp if it
-  // bounds them to eight tiles.
-  const int64_t items = (int64_t)L.n_groups * L.mult, tiles = L.keys / L.tile_keys;
+  // them all at once and the table bounds them to four tiles a warp (masks are then read with the tiles), else
+  // one after another per warp if it bounds them to eight tiles.
+  const int64_t items = (int64_t)pg.B * pg.Hkv * L.n_rb, tiles = L.keys / L.tile_keys;
   const int warps = paged_warps(pg.d, pg.bits, L.rows);
   L.mode = items <= 128 && tiles <= 4 * warps ? kPagedCoop : tiles <= 8 ? kPagedWhole : kPagedSplit;
+  L.plan = (r.lts || r.uts) && tiles > 0 && L.mode != kPagedCoop;
+  L.per_head = L.plan && r.Hm > 1;
+  L.n_groups = L.per_head ? pg.B * pg.Hkv : pg.B;
+  L.mult = L.per_head ? L.n_rb : pg.Hkv * L.n_rb;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t o = off; off = ws_align(off + bytes); return o; };
   if (L.mode == kPagedSplit) {
     const size_t slots = (size_t)2 * kPagedMaxCtas * warps;
     L.part = take(slots * L.rows * pg.d * 4);
     L.stat = take(slots * L.rows * 8);
     L.meta = take(slots / 2 * 8 * 4);
   }
-  if (masked) {
+  if (L.plan) {
     L.counts = take((size_t)L.n_groups * 4);
     L.list = take((size_t)L.n_groups * (L.keys / L.tile_keys) * 4);
     L.words = take((size_t)L.n_groups * L.n_words * L.keys * 4);
@@ -221,7 +221,7 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
   p.lte = r.lte;
   p.uts = r.uts;
   p.ute = r.ute;
-  const bool masked = L.masked;
+  const bool masked = r.lts || r.uts;
   p.Nq = r.Nq;
   p.Hq = r.Hq;
   p.Hm = masked ? r.Hm : 1;
@@ -256,7 +256,7 @@ int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_page
   p.stat = reinterpret_cast<float2*>(ws + L.stat);
   p.meta = reinterpret_cast<int*>(ws + L.meta);
   PlanOut plan{};
-  if (masked) {
+  if (L.plan) {
     p.counts = plan.counts = reinterpret_cast<int*>(ws + L.counts);
     p.list = plan.list = reinterpret_cast<int*>(ws + L.list);
     p.words = plan.words = reinterpret_cast<uint32_t*>(ws + L.words);

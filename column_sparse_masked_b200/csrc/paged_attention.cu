@@ -149,6 +149,47 @@ __device__ __forceinline__ Item item_of(const PagedAttnParams& p, int g, int in,
 }
 
 // ---------------------------------------------------------------------------
+// masks
+// ---------------------------------------------------------------------------
+// The rows of [r0, r0 + 32) that lie in [lo, hi), as a word.
+__device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t r0) {
+  const int a = (int)min(max(lo - r0, (int64_t)0), (int64_t)32), b = (int)min(max(hi - r0, (int64_t)0), (int64_t)32);
+  return bit_range(a, b);
+}
+
+// Which of rows [r0, r0 + 32) of a KV head see key j (j < hi), from the mask vectors.  Rows are numbered position
+// by position, the heads of one position together: an interval of positions is an interval of rows, of
+// which a mask head of its own has every G-th.
+__device__ __forceinline__ uint32_t seen_by(const PagedAttnParams& p, int b, int kvh, const Seq& seq, int j, int r0) {
+  const int64_t first = p.start ? (int64_t)p.start[b] : (int64_t)seq.first;  // as given: masks are applied literally
+  const bool own = p.Hm > 1;
+  uint32_t hid = p.causal ? rows_in(0, (j - first) * p.G, r0) : 0u;
+  if (j < p.Nm) {
+    for (int h = 0; h < (own ? p.G : 1); ++h) {
+      const int64_t m = ((int64_t)b * p.Hm + (own ? kvh * p.G + h : 0)) * p.Nm + j;
+      int lts = 0, lte = 0, uts = 0, ute = 0;
+      if (p.lts) {
+        lts = p.lts[m];
+        lte = p.lte[m];
+      }
+      if (p.uts) {
+        uts = p.uts[m];
+        ute = p.ute[m];
+      }
+      uint32_t mine = 0xffffffffu;  // rows of the head
+      if (own) {
+        mine = 0u;
+        const int at = p.div_g(r0) * p.G + h - r0;  // in (-G, G)
+        for (int r = at < 0 ? at + p.G : at; r < 32; r += p.G) mine |= 1u << r;
+      }
+      hid |= (rows_in((lts - first) * p.G, (lte - first) * p.G, r0) | rows_in((uts - first) * p.G, (ute - first) * p.G, r0)) &
+             mine;
+    }
+  }
+  return bit_range(0, min(32, p.Nq * p.G - r0)) & ~hid;
+}
+
+// ---------------------------------------------------------------------------
 // tiles and shared memory
 // ---------------------------------------------------------------------------
 template <int D, int BITS, int NT>
@@ -330,7 +371,7 @@ struct Issuer {
           if (page[i] >= 0) valid |= 1 << i;
         }
       }
-      if (valid != (1 << boxes) - 1) masked = 1;
+      if (valid != (1 << boxes) - 1 || (STEP > 1 && (p.lts || p.uts))) masked = 1;
     }
     flags = masked | (valid << 1);
     k += nb * STEP;
@@ -413,6 +454,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
   const int box_shift = min(p.pg.page_shift, KT == 32 ? 5 : 6);
   const uint32_t box_rows = 1u << box_shift;
   constexpr int STEP = COOP ? C::kWarps : 1;
+  const bool masks = p.lts || p.uts;
 
   // ---- Q fragments (B operand of S^T: k = values of the head, n = rows) ----
   // A lane's pieces of its row of each 8: for 4 bits values base + {0, 1} and base + {4, 5}, which
@@ -517,23 +559,32 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
       R = p.Nq * p.G - it.row0;
       fresh = false;
 #pragma unroll
-    for (int x = 0; x < 2 * NT; ++x) {
-      mx[x] = -INFINITY;
-      sum[x] = 0.f;
-      cor[x] = 0.f;
-    }
+      for (int x = 0; x < 2 * NT; ++x) {
+        mx[x] = -INFINITY;
+        sum[x] = 0.f;
+        cor[x] = 0.f;
+      }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
-
+          for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
     }
     const int stage = warp * C::kDepth + taken % C::kDepth;
     // row-visibility words of the thread's keys, asked for before the tile is waited for
     uint32_t seen[KT / 32 * 4];
-    if (p.words && ahead > 0 && k < wk.n && sm.hdr[stage].y) {
+    if (COOP && masks && ahead > 0 && k < wk.n) {
+      const int j0 = sm.hdr[stage].x;
+#pragma unroll
+      for (int y = 0; y < KT / 32; ++y) {
+        const int j = j0 + y * 32 + lane;
+        const uint32_t w = j < key_bound(p, seq) ? seen_by(p, it.b, it.kvh, seq, j, it.row0) : 0u;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) seen[y * 4 + x] = __shfl_sync(0xffffffffu, w, x * 8 + (BITS == 4 ? slot_key(g8) : g8));
+      }
+    }
+    if (!COOP && masks && ahead > 0 && k < wk.n && sm.hdr[stage].y) {
       const uint32_t* w = p.words + ((int64_t)wk.g * p.n_words + (it.row0 >> 5)) * p.words_stride + sm.hdr[stage].x;
 #pragma unroll
       for (int y = 0; y < KT / 32 * 4; ++y) seen[y] = w[(y >> 2) * 32 + (y & 3) * 8 + (BITS == 4 ? slot_key(g8) : g8)];
@@ -654,7 +705,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const int r = nt * 8 + 2 * q4 + e;
-                  const bool see = p.words ? (w >> r) & 1u
+                  const bool see = masks ? (w >> r) & 1u
                                            : j < seq.len && (!p.causal || j <= seq.first + p.div_g(it.row0 + r));
                   if (!(see && there)) {
                     hid |= 1u << ((m2 * 2 + hf) * 2 * NT + nt * 2 + e);
@@ -823,11 +874,11 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
       if (BITS == 4) copy_commit();
       ++ahead;
     }
+    __syncwarp();  // the headers of the tiles just asked for
     if (k < wk.n) continue;
     k -= wk.n;
 
     // ---- the segment's end ----
-
 #pragma unroll
     for (int x = 0; x < 2 * NT; ++x) {
       sum[x] = sum8(sum[x]);
@@ -1228,12 +1279,6 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
 // group that does both in one launch took 30 us for one sequence of 128K keys:
 // 8 SMs do not have enough loads in flight for 2 MB of vectors.
 // ---------------------------------------------------------------------------
-// The rows of [r0, r0 + 32) that lie in [lo, hi), as a word.
-__device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t r0) {
-  const int a = (int)min(max(lo - r0, (int64_t)0), (int64_t)32), b = (int)min(max(hi - r0, (int64_t)0), (int64_t)32);
-  return bit_range(a, b);
-}
-
 template <int KT>
 __global__ void __launch_bounds__(256) paged_plan_kernel(const __grid_constant__ PagedAttnParams p, PlanOut out) {
   griddep_wait();
@@ -1242,53 +1287,17 @@ __global__ void __launch_bounds__(256) paged_plan_kernel(const __grid_constant__
   const int g = x / p.list_stride, t = x - g * p.list_stride;
   if (g >= p.n_groups) return;
   const int b = group_batch(p, g);
-  const int hm0 = p.per_head ? (g - b * p.pg.Hkv) * p.G : 0, nh = p.per_head ? p.G : 1;
   const Seq seq = load_seq(p, b);
-  const int hi = key_bound(p, seq), R = p.Nq * p.G;
-  const int64_t first = p.start ? (int64_t)p.start[b] : (int64_t)seq.first;  // as given: masks are applied literally
+  const int hi = key_bound(p, seq);
   if (t * KT >= hi) return;
-  // Rows are numbered position by position, the heads of one position together: an interval of positions is
-  // an interval of rows, of which a head has every G-th.
-  auto rows_hidden = [&](int64_t lo, int64_t end, int r0) { return rows_in((lo - first) * p.G, (end - first) * p.G, r0); };
   bool any = false, all = true;
 #pragma unroll 1
   for (int w = 0; w < p.n_words; ++w) {
-    const int r0 = 32 * w;
-    const uint32_t rows = bit_range(0, min(32, R - r0));
-    uint32_t hid[KT / 32] = {};
-    for (int h = 0; h < nh; ++h) {
-      uint32_t mine = 0xffffffffu;  // rows of the head
-      if (p.per_head) {
-        mine = 0u;
-        for (int r = h - r0 % p.G; r < 32; r += p.G)
-          if (r >= 0) mine |= 1u << r;
-      }
-      int4 v[KT / 32];
-#pragma unroll
-      for (int y = 0; y < KT / 32; ++y) {
-        const int j = t * KT + y * 32 + lane;
-        const int64_t m = ((int64_t)b * p.Hm + hm0 + h) * p.Nm + j;
-        v[y] = make_int4(0, 0, 0, 0);
-        if (j < p.Nm && j < hi) {
-          if (p.lts) {
-            v[y].x = p.lts[m];
-            v[y].y = p.lte[m];
-          }
-          if (p.uts) {
-            v[y].z = p.uts[m];
-            v[y].w = p.ute[m];
-          }
-        }
-      }
-#pragma unroll
-      for (int y = 0; y < KT / 32; ++y)
-        hid[y] |= (rows_hidden(v[y].x, v[y].y, r0) | rows_hidden(v[y].z, v[y].w, r0)) & mine;
-    }
+    const uint32_t rows = bit_range(0, min(32, p.Nq * p.G - 32 * w));
 #pragma unroll
     for (int y = 0; y < KT / 32; ++y) {
       const int j = t * KT + y * 32 + lane;
-      if (p.causal) hid[y] |= rows_hidden(first, j, r0);
-      const uint32_t see = j < hi ? rows & ~hid[y] : 0u;
+      const uint32_t see = j < hi ? seen_by(p, b, p.per_head ? g - b * p.pg.Hkv : 0, seq, j, 32 * w) : 0u;
       out.words[((int64_t)g * p.n_words + w) * p.words_stride + j] = see;
       any |= see != 0;
       all &= see == rows;
