@@ -85,22 +85,41 @@ struct PagedLayout {
   size_t part, stat, meta, counts, list, words, flags, bytes;
 };
 
+constexpr int kSms = 148;  // of a B200: workspace sizes must not depend on the current device
+
 PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& r) {
   PagedLayout L{};
   const int64_t R = (int64_t)r.Nq * (r.Hq / pg.Hkv);
-  L.rows = R <= 8 ? 8 : R <= 16 ? 16 : 32;
-  L.n_rb = (int)((R + L.rows - 1) / L.rows);
   L.tile_keys = paged_tile_keys(pg.d, pg.bits);
   L.n_words = (int)((R + 31) / 32);
   const int64_t cap = (int64_t)pg.table_width * pg.page_size;
   L.keys = (cap + L.tile_keys - 1) / L.tile_keys * L.tile_keys;
-  // Whole items where cutting has nothing to give, and no second kernel: one per CTA if the device takes
-  // them all at once and the table bounds them to four tiles a warp (masks are then read with the tiles), else
-  // one after another per warp if it bounds them to eight tiles.
-  const int64_t items = (int64_t)pg.B * pg.Hkv * L.n_rb, tiles = L.keys / L.tile_keys;
+  const int64_t tiles = L.keys / L.tile_keys;
+  const bool masked = r.lts || r.uts;
+  auto blocks = [&](int rows) { return (R + rows - 1) / rows; };
+  // Rows of a block.  A block reads its keys once, so the fewest blocks read least; but blocks of 32 rows run
+  // with 4 warps an SM and a long way through cold instructions.  bf16, 32 rows over 32 sequences of 4K keys: blocks
+  // of 32 take 145 us, of 16 188, of 8 331; over 8 sequences 59, 48 and 61; with masks that hide three
+  // quarters 70, 61 and 76 over 32, 34, 30 and 30 over 8.  In 4 bits the codes' conversion counts and not the bytes: 32
+  // rows over 32 sequences take 125 us in blocks of 16, 153 in blocks of 8 and 167 in blocks of 32.
+  const bool wide = pg.bits == 16 && !masked && blocks(32) * pg.B * pg.Hkv * tiles >= 24 * 4 * kSms;  // 24 tiles a warp
+  L.rows = R <= 8 ? 8 : R <= 16 || !wide ? 16 : 32;
+  // Whole items where cutting has nothing to give, and no second kernel.  One per CTA if the table bounds them to
+  // four tiles a warp and the device takes them all at once, in the smallest blocks of rows for which it
+  // does (4 sequences of 103 keys and 32 rows: 10.7 us in blocks of 32, 6.8 in blocks of 8); masks are then read with
+  // the tiles, without a plan.  One after another per warp if the table bounds them to eight tiles (20
+  // sequences of 110 keys: 10 us, 16 with four waves of CTAs).  Else cut, unless two waves of CTAs take them
+  // (30 sequences of 1079 keys with masks, 4 bits: 22 us, cut 32; 21 of 385 keys without: 11.0 and 11.9).
+  L.mode = tiles <= 8 ? kPagedWhole : kPagedSplit;
+  for (int waves = 1; waves <= (tiles <= 8 ? 1 : 2) && L.mode != kPagedCoop; ++waves)
+    for (int rows = 8; rows <= (pg.bits == 16 ? 32 : 16) && L.mode != kPagedCoop; rows *= 2)
+      if (blocks(rows) * pg.B * pg.Hkv <= waves * kSms && tiles <= 4 * paged_warps(pg.d, pg.bits, rows)) {
+        L.mode = kPagedCoop;
+        L.rows = rows;
+      }
+  L.n_rb = (int)blocks(L.rows);
   const int warps = paged_warps(pg.d, pg.bits, L.rows);
-  L.mode = items <= 128 && tiles <= 4 * warps ? kPagedCoop : tiles <= 8 ? kPagedWhole : kPagedSplit;
-  L.plan = (r.lts || r.uts) && tiles > 0 && L.mode != kPagedCoop;
+  L.plan = masked && tiles > 0 && L.mode != kPagedCoop;
   L.per_head = L.plan && r.Hm > 1;
   L.n_groups = L.per_head ? pg.B * pg.Hkv : pg.B;
   L.mult = L.per_head ? L.n_rb : pg.Hkv * L.n_rb;
@@ -114,9 +133,9 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
   }
   if (L.plan) {
     L.counts = take((size_t)L.n_groups * 4);
-    L.list = take((size_t)L.n_groups * (L.keys / L.tile_keys) * 4);
+    L.list = take((size_t)L.n_groups * tiles * 4);
     L.words = take((size_t)L.n_groups * L.n_words * L.keys * 4);
-    L.flags = take((size_t)L.n_groups * (L.keys / L.tile_keys));
+    L.flags = take((size_t)L.n_groups * tiles);
   }
   L.bytes = off > 0 ? off : 256;
   return L;

@@ -151,42 +151,50 @@ __device__ __forceinline__ Item item_of(const PagedAttnParams& p, int g, int in,
 // ---------------------------------------------------------------------------
 // masks
 // ---------------------------------------------------------------------------
-// The rows of [r0, r0 + 32) that lie in [lo, hi), as a word.
-__device__ __forceinline__ uint32_t rows_in(int64_t lo, int64_t hi, int64_t r0) {
-  const int a = (int)min(max(lo - r0, (int64_t)0), (int64_t)32), b = (int)min(max(hi - r0, (int64_t)0), (int64_t)32);
-  return bit_range(a, b);
-}
-
-// Which of rows [r0, r0 + 32) of a KV head see key j (j < hi), from the mask vectors.  Rows are numbered position
-// by position, the heads of one position together: an interval of positions is an interval of rows, of
-// which a mask head of its own has every G-th.
+// Which of the ROWS rows of a KV head from r0 on see key j (j < hi), from the mask vectors, as a word.  Rows are
+// numbered position by position, the heads of one position together: an interval of positions is an
+// interval of rows, of which a mask head of its own has every G-th.
+template <int ROWS>
 __device__ __forceinline__ uint32_t seen_by(const PagedAttnParams& p, int b, int kvh, const Seq& seq, int j, int r0) {
-  const int64_t first = p.start ? (int64_t)p.start[b] : (int64_t)seq.first;  // as given: masks are applied literally
-  const bool own = p.Hm > 1;
-  uint32_t hid = p.causal ? rows_in(0, (j - first) * p.G, r0) : 0u;
+  const int first = p.start ? p.start[b] : seq.first;  // as given: masks are applied literally
+  // the word's first row at or after position `pos` (saturated: boundaries and starts are any 32-bit numbers)
+  auto row_at = [&](int pos) {
+    int i;
+    asm("sub.sat.s32 %0, %1, %2;" : "=r"(i) : "r"(pos), "r"(first));
+    return min(max(min(max(i, 0), p.Nq) * p.G - r0, 0), ROWS);
+  };
+  uint32_t hid = p.causal ? bit_range(0, row_at(j)) : 0u;
   if (j < p.Nm) {
-    for (int h = 0; h < (own ? p.G : 1); ++h) {
-      const int64_t m = ((int64_t)b * p.Hm + (own ? kvh * p.G + h : 0)) * p.Nm + j;
-      int lts = 0, lte = 0, uts = 0, ute = 0;
-      if (p.lts) {
-        lts = p.lts[m];
-        lte = p.lte[m];
+    if (p.Hm == 1) {
+      const int64_t m = (int64_t)b * p.Nm + j;
+      const int a0 = p.lts ? p.lts[m] : 0, a1 = p.lts ? p.lte[m] : 0, a2 = p.uts ? p.uts[m] : 0, a3 = p.uts ? p.ute[m] : 0;
+      hid |= bit_range(row_at(a0), row_at(a1)) | bit_range(row_at(a2), row_at(a3));
+    } else {
+      const int heads = min(p.G, ROWS), h0 = r0 - p.div_g(r0) * p.G;  // heads of rows r0, r0 + 1, ...
+      const int64_t base = ((int64_t)b * p.Hm + kvh * p.G) * p.Nm + j;
+      for (int x0 = 0; x0 < heads; x0 += 4) {  // the vectors of four heads are asked for together
+        int v[4][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int h = h0 + x0 + x;
+          const int64_t m = base + (int64_t)(h < p.G ? h : h - p.G) * p.Nm;
+          const bool in = x0 + x < heads;
+          v[x][0] = in && p.lts ? p.lts[m] : 0;
+          v[x][1] = in && p.lts ? p.lte[m] : 0;
+          v[x][2] = in && p.uts ? p.uts[m] : 0;
+          v[x][3] = in && p.uts ? p.ute[m] : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (x0 + x >= heads) break;
+          uint32_t mine = 0u;  // rows of the head
+          for (int r = x0 + x; r < ROWS; r += p.G) mine |= 1u << r;
+          hid |= (bit_range(row_at(v[x][0]), row_at(v[x][1])) | bit_range(row_at(v[x][2]), row_at(v[x][3]))) & mine;
+        }
       }
-      if (p.uts) {
-        uts = p.uts[m];
-        ute = p.ute[m];
-      }
-      uint32_t mine = 0xffffffffu;  // rows of the head
-      if (own) {
-        mine = 0u;
-        const int at = p.div_g(r0) * p.G + h - r0;  // in (-G, G)
-        for (int r = at < 0 ? at + p.G : at; r < 32; r += p.G) mine |= 1u << r;
-      }
-      hid |= (rows_in((lts - first) * p.G, (lte - first) * p.G, r0) | rows_in((uts - first) * p.G, (ute - first) * p.G, r0)) &
-             mine;
     }
   }
-  return bit_range(0, min(32, p.Nq * p.G - r0)) & ~hid;
+  return bit_range(0, min(ROWS, p.Nq * p.G - r0)) & ~hid;
 }
 
 // ---------------------------------------------------------------------------
@@ -207,7 +215,7 @@ struct Cfg {
   static constexpr int kMerge = kWarps * kRows * kStride * 4;   // on top of the rings
   static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;  // per warp
   static constexpr int kPerStage = kStage + 16 + 8;             // + header, barrier
-  static constexpr int kFixed = kWarps * (kQBytes + 4 * kRows * 4) + kSeqCache * 12 + 1024 + 256;
+  static constexpr int kFixed = kWarps * (kQBytes + 3 * kRows * 4) + kSeqCache * 12 + 1024 + 256;
   // Every warp has a ring of its own, which it fills and empties itself: a stage is refilled by the warp
   // that has just read it, so nothing waits for another warp.
   static constexpr int kFit = (225 * 1024 - kFixed) / kPerStage / kWarps;
@@ -227,7 +235,6 @@ struct Smem {
   uint64_t* full;      // kStages
   uint2* q;            // Q fragments of each warp (kQShared)
   float *m, *l, *c;    // kWarps x kRows (one item per CTA)
-  float* qsum;         // kWarps x kRows
   Seq* seq;            // kSeqCache
   int* counts;         // kSeqCache
   int* abort;
@@ -241,7 +248,6 @@ struct Smem {
     m = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
     l = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
     c = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
-    qsum = reinterpret_cast<float*>(x); x += C::kWarps * C::kRows * 4;
     seq = reinterpret_cast<Seq*>(x); x += kSeqCache * 8;
     counts = reinterpret_cast<int*>(x); x += kSeqCache * 4;
     abort = reinterpret_cast<int*>(x);
@@ -472,66 +478,44 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g8;
       const __nv_bfloat16* src = row_ptr(it, min(r, R - 1));
+      uint2 v[KS];  // all of them asked for before the first is stored
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         const uint32_t* a = reinterpret_cast<const uint32_t*>(
             BITS == 16 ? src + ks * 16 + 2 * q4 : src + (D / 4) * q4 + 8 * (ks >> 1) + 2 * (ks & 1));
-        uint2 v = make_uint2(a[0], a[BITS == 16 ? 4 : 2]);
-        if (C::kQShared) {
-          if (r >= R) v = make_uint2(0u, 0u);
-          qw[(ks * NT + nt) * 32 + lane] =
-              BITS == 16 ? v : make_uint2(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632));
-        } else {
-          qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt] = v;
-        }
+        v[ks] = make_uint2(a[0], a[BITS == 16 ? 4 : 2]);
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if constexpr (C::kQShared) qw[(ks * NT + nt) * 32 + lane] = r < R ? v[ks] : make_uint2(0u, 0u);
+        else qf[ks][nt] = v[ks];
       }
     }
   };
   auto turn_q = [&](const Item& it) {
-    const int R = p.Nq * p.G - it.row0;
-    if (C::kQShared) {
-      if (BITS == 4) {
-        float s = 0.f;
-        if (lane < C::kRows && lane < R) {
-          const uint4* src = reinterpret_cast<const uint4*>(row_ptr(it, lane));
-#pragma unroll 2
-          for (int x = 0; x < D / 8; ++x) {
-            const uint4 u = src[x];
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (C::kQShared) {
+      __syncwarp();
+    } else {
+      const int R = p.Nq * p.G - it.row0;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) s += __uint_as_float(w[y] << 16) + __uint_as_float(w[y] & 0xffff0000u);
+      for (int nt = 0; nt < NT; ++nt) {
+        float s = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint2& u = qf[ks][nt];
+          if (nt * 8 + g8 >= R) u = make_uint2(0u, 0u);
+          if (BITS == 4) {
+            u = make_uint2(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.x, u.y, 0x7632));
+            s += (__uint_as_float(u.x << 16) + __uint_as_float(u.x & 0xffff0000u)) +
+                 (__uint_as_float(u.y << 16) + __uint_as_float(u.y & 0xffff0000u));
           }
         }
-        if (lane < C::kRows) sm.qsum[warp * C::kRows + lane] = s;
-      }
-      __syncwarp();
-      if (BITS == 4) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          qsum[2 * nt] = sm.qsum[warp * C::kRows + nt * 8 + 2 * q4];
-          qsum[2 * nt + 1] = sm.qsum[warp * C::kRows + nt * 8 + 2 * q4 + 1];
-        }
-      }
-      return;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float s = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uint2& u = qf[C::kQShared ? 0 : ks][C::kQShared ? 0 : nt];
-        if (nt * 8 + g8 >= R) u = make_uint2(0u, 0u);
         if (BITS == 4) {
-          u = make_uint2(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.x, u.y, 0x7632));
-          s += (__uint_as_float(u.x << 16) + __uint_as_float(u.x & 0xffff0000u)) +
-               (__uint_as_float(u.y << 16) + __uint_as_float(u.y & 0xffff0000u));
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);  // lanes of row g8 hold its sum
+          qsum[2 * nt] = __shfl_sync(0xffffffffu, s, 8 * q4);
+          qsum[2 * nt + 1] = __shfl_sync(0xffffffffu, s, 8 * q4 + 4);
         }
-      }
-      if (BITS == 4) {
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);  // lanes of row g8 hold its sum
-        qsum[2 * nt] = __shfl_sync(0xffffffffu, s, 8 * q4);
-        qsum[2 * nt + 1] = __shfl_sync(0xffffffffu, s, 8 * q4 + 4);
       }
     }
   };
@@ -579,7 +563,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
 #pragma unroll
       for (int y = 0; y < KT / 32; ++y) {
         const int j = j0 + y * 32 + lane;
-        const uint32_t w = j < key_bound(p, seq) ? seen_by(p, it.b, it.kvh, seq, j, it.row0) : 0u;
+        const uint32_t w = j < key_bound(p, seq) ? seen_by<C::kRows>(p, it.b, it.kvh, seq, j, it.row0) : 0u;
 #pragma unroll
         for (int x = 0; x < 4; ++x) seen[y * 4 + x] = __shfl_sync(0xffffffffu, w, x * 8 + (BITS == 4 ? slot_key(g8) : g8));
       }
@@ -587,7 +571,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
     if (!COOP && masks && ahead > 0 && k < wk.n && sm.hdr[stage].y) {
       const uint32_t* w = p.words + ((int64_t)wk.g * p.n_words + (it.row0 >> 5)) * p.words_stride + sm.hdr[stage].x;
 #pragma unroll
-      for (int y = 0; y < KT / 32 * 4; ++y) seen[y] = w[(y >> 2) * 32 + (y & 3) * 8 + (BITS == 4 ? slot_key(g8) : g8)];
+      for (int y = 0; y < KT / 32 * 4; ++y) seen[y] = w[(y >> 2) * 32 + (y & 3) * 8 + (BITS == 4 ? slot_key(g8) : g8)] >> (it.row0 & 31);
     }
     if (BITS == 16 && ahead > 0 && k < wk.n) {
       if (alive) alive = mbar_wait(&sm.full[stage], (taken / C::kDepth) & 1u, wc);
@@ -1297,7 +1281,7 @@ __global__ void __launch_bounds__(256) paged_plan_kernel(const __grid_constant__
 #pragma unroll
     for (int y = 0; y < KT / 32; ++y) {
       const int j = t * KT + y * 32 + lane;
-      const uint32_t see = j < hi ? seen_by(p, b, p.per_head ? g - b * p.pg.Hkv : 0, seq, j, 32 * w) : 0u;
+      const uint32_t see = j < hi ? seen_by<32>(p, b, p.per_head ? g - b * p.pg.Hkv : 0, seq, j, 32 * w) : 0u;
       out.words[((int64_t)g * p.n_words + w) * p.words_stride + j] = see;
       any |= see != 0;
       all &= see == rows;
@@ -1378,9 +1362,10 @@ static cudaError_t launch_rows(const PagedAttnParams& p, const CUtensorMap& tk, 
   const bool coop = p.mode == kPagedCoop;
   if (p.rows == 8)
     return coop ? launch_variant<D, BITS, 1, true>(p, tk, tv, grid, st) : launch_variant<D, BITS, 1, false>(p, tk, tv, grid, st);
-  if (p.rows == 16)
-    return coop ? launch_variant<D, BITS, 2, true>(p, tk, tv, grid, st) : launch_variant<D, BITS, 2, false>(p, tk, tv, grid, st);
-  return coop ? launch_variant<D, BITS, 4, true>(p, tk, tv, grid, st) : launch_variant<D, BITS, 4, false>(p, tk, tv, grid, st);
+  if constexpr (BITS == 16)  // (4 bits: blocks of at most 16 rows)
+    if (p.rows == 32)
+      return coop ? launch_variant<D, BITS, 4, true>(p, tk, tv, grid, st) : launch_variant<D, BITS, 4, false>(p, tk, tv, grid, st);
+  return coop ? launch_variant<D, BITS, 2, true>(p, tk, tv, grid, st) : launch_variant<D, BITS, 2, false>(p, tk, tv, grid, st);
 }
 
 int paged_tile_keys(int d, int bits) { return bits == 16 && d == 128 ? 32 : 64; }
