@@ -57,10 +57,11 @@ inline FastDiv fast_div(int d) {
 // CTA per item.
 enum PagedMode { kPagedSplit = 0, kPagedWhole = 1, kPagedCoop = 2 };
 
-// Warps of an attention CTA (one per SM).  Registers allow 7 at 255 a thread and 12 at 168; the rings of
-// tiles in shared memory allow 12 tiles of 16 KiB, 24 of 8.5 KiB.
+// Warps of an attention CTA (one per SM).  Registers allow 8 at 255 a thread and 12 at 168; the rings of
+// tiles in shared memory allow 12 tiles of 16 KiB (two for each of 6 warps, three for 4 with their rows of Q), 24 of
+// 8.5 KiB.  Blocks of 32 rows are for bf16 alone.
 __host__ __device__ constexpr int paged_warps(int d, int bits, int rows) {
-  return bits == 16 ? (rows == 32 ? 4 : 6) : (rows == 32 ? 6 : rows == 16 ? 8 : 12);
+  return bits == 16 ? (rows == 32 ? 4 : 6) : (rows == 16 ? 8 : 12);
 }
 
 struct PagedAttnParams {

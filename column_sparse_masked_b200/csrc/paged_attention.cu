@@ -1011,6 +1011,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
     WaitCtx w2 = wc;
     int zero = 0;
     w2.abort = &zero;
+    w2.limit_ns = max(wc.limit_ns, (uint64_t)1000000000);
     for (int i = taken; i < is.issued; ++i)
       mbar_wait(&sm.full[warp * C::kDepth + i % C::kDepth], (i / C::kDepth) & 1u, w2);
   }

@@ -237,6 +237,54 @@ def test_attention_many_short_sequences(bits, Hm, cap):
 
 
 @pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("Hm", [0, 1, 8])
+@pytest.mark.parametrize("shape", ["short", "two_waves", "many", "long", "wide_table"])
+def test_attention_more_rows_than_a_block(bits, Hm, shape):
+    """40 rows of a KV head: several blocks of rows, of 8, 16 and (bf16 with room for long sequences) 32, one
+    item per CTA, per warp, and cut."""
+    d, Nq, width = 128, 10, None
+    lens = {"short": [61, 200], "two_waves": [600] + [9] * 59, "many": [120, 3] * 20, "long": [5100, 40],
+            "wide_table": [700, 90]}[shape]
+    if shape == "wide_table":
+        width = 1800
+    if shape in ("two_waves", "many"):
+        Nq, d = 5, 64 if shape == "many" else 128
+    cache = Cache(26, lens, 2, d, 64, bits, width=width).cuda()
+    vec = (None,) * 4 if Hm == 0 else masks("random", len(lens), Hm, max(lens), 15, Nq)
+    check_attention(case_q(len(lens), Nq, 8, d), cache, lens, vec)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("Hm,width", [(0, None), (1, None), (2, None), (0, 48), (1, 48), (2, 48)])
+def test_attention_more_sequences_than_shared_memory_holds(bits, Hm, width):
+    rng = np.random.default_rng(6)
+    lens = [int(x) for x in rng.integers(0, 70, 700)]
+    lens[0] = lens[511] = lens[699] = 0
+    if width:
+        lens[5], lens[512], lens[698] = 700, 650, 300
+    cache = Cache(27, lens, 2, 64, 16, bits, width=width).cuda()
+    vec = (None,) * 4 if Hm == 0 else masks("random", 700, Hm, max(lens), 7, 1)
+    check_attention(case_q(700, 1, 2, 64), cache, lens, vec)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("width", [None, 80])
+def test_attention_positions_at_the_ends_of_their_type(bits, width):
+    """start and boundaries anywhere in 32 bits: positions do not wrap."""
+    lens, lo, hi = [90, 40, 77, 5], -2 ** 31, 2 ** 31 - 1
+    cache, q = Cache(28, lens, 1, 64, 16, bits, width=width).cuda(), case_q(4, 4, 2, 64)
+    rng = np.random.default_rng(8)
+    for starts in ([hi, hi - 2, lo, lo + 1], [2 ** 30, 2 ** 30 + 5, -2 ** 30, -2 ** 30 - 1], [hi - 1, 3, -1, 0]):
+        near = np.array(starts)[None, :, None, None] + rng.integers(-3, 8, (4, 4, 1, 90))
+        ends = rng.choice([lo, lo + 1, -1, 0, 1, hi - 1, hi], (4, 4, 1, 90))
+        vec = np.clip(np.where(rng.random((4, 4, 1, 90)) < 0.7, near, ends), lo, hi)
+        vec = [torch.from_numpy(x.astype(np.int32)).cuda() for x in vec]
+        for causal in (False, True):
+            check_attention(q, cache, lens, vec, start=i32(starts), causal=causal)
+            check_attention(q, cache, lens, start=i32(starts), causal=causal)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
 def test_attention_long(bits):
     """One long sequence split over the whole device; every page also checked through its weights: keys are equal,
     so O is the mean of the values."""

@@ -1,6 +1,7 @@
 """The paged-cache entry points reject malformed arguments before any launch (CPU only): the
 Python binding by exceptions, the C ABI by error codes."""
 import ctypes
+import sys
 
 import pytest
 import torch
@@ -250,3 +251,13 @@ def test_c_empty_calls_touch_no_device(library):
     assert library.flashmask_paged_append(ctypes.byref(c_pages()), ctypes.byref(c_append(N=0)), None) == 0
     assert library.flashmask_paged_gather(ctypes.byref(c_pages()), None, 0, None, None, None) == 0
     assert library.flashmask_paged_attention(ctypes.byref(c_pages()), ctypes.byref(c_rows(Nq=0)), None, 0, None) == 0
+
+
+def test_missing_binding_is_named(monkeypatch):
+    from column_sparse_masked_b200 import paged
+
+    monkeypatch.setattr(paged, "_calls", None)
+    monkeypatch.setitem(sys.modules, "column_sparse_masked_b200._paged_binding", None)
+    monkeypatch.delattr(fm, "_paged_binding", raising=False)
+    with pytest.raises(RuntimeError, match="_paged_binding.so is missing"):
+        fm.paged_gather(None, None, None, None, 1)
