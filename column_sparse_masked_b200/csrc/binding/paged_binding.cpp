@@ -73,6 +73,7 @@ bool pages(T k, T v, T ks, T vs, T table, flashmask_pages* p) {
     return false;
   for (int64_t x : {s[0], s[1], s[2], 2 * s[3], table->size(0), table->size(1)})
     if (!small(x)) return false;
+  if (s[1] == 0) return false;
   p->k = k->data_ptr();
   p->v = v->data_ptr();
   p->k_scales = ptr(ks);

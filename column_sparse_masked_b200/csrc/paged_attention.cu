@@ -319,11 +319,19 @@ __device__ __forceinline__ uint32_t centred(uint32_t x, int i) {
 // parity.  Any permutation gives the same sums.
 __device__ __forceinline__ int slot_key(int s) { return (s & 1) ? 4 + ((s >> 1) ^ 1) : s >> 1; }
 
+// The larger value, NaN if either is: a row with a score of NaN keeps a maximum of NaN, and is not taken for one
+// that saw nothing.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Largest value over the 8 lanes that share lane % 4.
 __device__ __forceinline__ float max8(float x) {
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+  x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return max_nan(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
 __device__ __forceinline__ float sum8(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 4);
@@ -705,9 +713,9 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float x = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
-            mn[2 * nt + e] = fmaxf(mx[2 * nt + e], max8(x));
-            grew |= mn[2 * nt + e] > mx[2 * nt + e];
+            const float x = max_nan(max_nan(s[0][nt][e], s[0][nt][2 + e]), max_nan(s[1][nt][e], s[1][nt][2 + e]));
+            mn[2 * nt + e] = max_nan(mx[2 * nt + e], max8(x));
+            grew |= !(mn[2 * nt + e] <= mx[2 * nt + e]);
           }
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -886,7 +894,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
         const int r = (x >> 1) * 8 + 2 * q4 + (x & 1);
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, sm.m[w * C::kRows + r]);
+        for (int w = 0; w < C::kWarps; ++w) top = max_nan(top, sm.m[w * C::kRows + r]);
         const float f = mx[x] == -INFINITY ? 0.f : fast_exp2((mx[x] - top) * p.scale_log2);
         float* dst = merge + (warp * C::kRows + r) * C::kStride;
 #pragma unroll
@@ -905,7 +913,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
         const int r = x / (D / 4), d4 = x % (D / 4);
         float top = -INFINITY, L = 0.f, cc = 0.f;
 #pragma unroll
-        for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, sm.m[w * C::kRows + r]);
+        for (int w = 0; w < C::kWarps; ++w) top = max_nan(top, sm.m[w * C::kRows + r]);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
@@ -1159,8 +1167,8 @@ __device__ __forceinline__ Joined join(const PagedAttnParams& p, int run, int fi
     const float2 ml = mine < parts ? p.stat[slot(mine) * ROWS + r] : make_float2(-INFINITY, 0.f);
     float top = ml.x;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    top = fmaxf(top, j.m);
+    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = max_nan(top, j.m);
     const float f = j.m == -INFINITY ? 0.f : fast_exp2((j.m - top) * p.scale_log2);
     const float w = ml.x == -INFINITY ? 0.f : fast_exp2((ml.x - top) * p.scale_log2);
     float l = ml.y * w;
@@ -1241,7 +1249,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
     if (warp != 0) continue;
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, ms[i]);
+    for (int i = 0; i < 8; ++i) top = max_nan(top, ms[i]);
     Joined all{top, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

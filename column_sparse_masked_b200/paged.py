@@ -88,6 +88,8 @@ def _pages(k_pages, v_pages, k_scales, v_scales, block_table, B=None, d=None, Hk
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("k_pages must be a 4-D tensor [P, Hkv, page_size, d]")
     P, H, page, last = k_pages.shape
+    if H == 0:
+        raise ValueError("k_pages must have at least one head")
     if k_pages.dtype is _U8:
         width = 2 * last
         _is("k_scales", k_scales, _BF16, (P, H, page, 2))

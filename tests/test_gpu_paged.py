@@ -174,6 +174,59 @@ def test_attention_nan_reaches_only_rows_that_see_it(Nq):
     assert torch.equal(o[:, :, 1:], ro[:, :, 1:])
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("lens,width,B", [([150], None, 1), ([60] * 90, None, 90), ([3000, 40], 60, 2)])
+def test_attention_nan_scores_are_not_taken_for_hidden_ones(bits, lens, width, B):
+    """A row of q with a NaN, and a key of NaN that every row of one KV head sees, give NaN in O and LSE of those rows
+    and leave the others alone: one item per CTA, per warp, and cut."""
+    cache, q = Cache(29, lens, 2, 64, 64, bits, width=width), case_q(B, 2, 4, 64)
+    clean = Cache(29, lens, 2, 64, 64, bits, width=width).cuda()
+    want, wl_ = fm.paged_attention(q, clean.k, clean.v, clean.table, i32(lens), **clean.kw)
+    bad_q = q.clone()
+    bad_q[0, 1, 2, 5] = float("nan")
+    o, lse = fm.paged_attention(bad_q, clean.k, clean.v, clean.table, i32(lens), **clean.kw)
+    assert torch.isnan(o[0, 1, 2]).all() and torch.isnan(lse[0, 2, 1])
+    o[0, 1, 2], lse[0, 2, 1] = want[0, 1, 2], wl_[0, 2, 1]
+    assert torch.equal(o, want) and torch.equal(lse, wl_)
+    (cache.k if bits == 16 else cache.ks)[int(cache.table[0, 0]), 1, 3] = float("nan")
+    cache = cache.cuda()
+    o, lse = fm.paged_attention(q, cache.k, cache.v, cache.table, i32(lens), **cache.kw)
+    assert torch.isnan(o[0, :, 2:]).all() and torch.isnan(lse[0, 2:]).all()
+    assert torch.equal(o[0, :, :2], want[0, :, :2]) and torch.equal(o[1:], want[1:]) and torch.equal(lse[1:], wl_[1:])
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_cache_of_more_than_32_bits(bits):
+    """Pages whose offsets pass 2^32 bytes and, for bf16, 2^31 values: the last pages of the cache and the first ones
+    give what the same pages give in a small cache."""
+    Hkv, page, d, lens = 2, 256, 128, [700, 300]
+    small = Cache(30, lens, Hkv, d, page, bits, spare=0).cuda()
+    P = (2 ** 24 if bits == 16 else 2 ** 26) // (Hkv * page) + 8
+    big = [None if x is None else torch.empty((P,) + x.shape[1:], dtype=x.dtype, device="cuda")
+           for x in (small.k, small.v, small.ks, small.vs)]
+    assert big[0].numel() * big[0].element_size() > 2 ** 32
+    n = small.k.shape[0]
+    where = torch.tensor([P - 1, 0, P - 2, P - 5, 1, P - 3][:n], device="cuda")
+    for x, y in zip(big, (small.k, small.v, small.ks, small.vs)):
+        if x is not None:
+            x[where] = y
+    table = torch.where(small.table < 0, -1, where[small.table.clamp(min=0).long()]).int()
+    kw = {} if bits == 16 else {"k_scales": big[2], "v_scales": big[3]}
+    q, lens_ = case_q(2, 3, 8, d), i32(lens)
+    for a, b in zip(fm.paged_attention(q, big[0], big[1], table, lens_, **kw),
+                    fm.paged_attention(q, small.k, small.v, small.table, lens_, **small.kw)):
+        assert torch.equal(a, b)
+    for a, b in zip(fm.paged_gather(big[0], big[1], table, lens_, 700, **kw),
+                    fm.paged_gather(small.k, small.v, small.table, lens_, 700, **small.kw)):
+        assert torch.equal(a, b)
+    k = case_q(2, 5, Hkv, d, 3)
+    fm.paged_append(k, k, big[0], big[1], table, i32([250, 290]), **kw)
+    fm.paged_append(k, k, small.k, small.v, small.table, i32([250, 290]), **small.kw)
+    for x, y in zip(big, (small.k, small.v, small.ks, small.vs)):
+        if x is not None:
+            assert torch.equal(x[where], y)
+
+
 def test_attention_infinite_value_in_a_seen_key():
     n = 100
     cache, q = Cache(16, [n], 1, 64, 16, 16), case_q(1, 1, 2, 64)

@@ -261,3 +261,14 @@ def test_missing_binding_is_named(monkeypatch):
     monkeypatch.delattr(fm, "_paged_binding", raising=False)
     with pytest.raises(RuntimeError, match="_paged_binding.so is missing"):
         fm.paged_gather(None, None, None, None, 1)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_pages_without_heads_are_refused(bits):
+    a = args(bits)
+    for n in ("k_pages", "v_pages", "k_scales", "v_scales"):
+        if a[n] is not None:
+            a[n] = a[n][:, :0]
+    for call in (append, attend):
+        with pytest.raises(ValueError, match="at least one head"):
+            call(a)
