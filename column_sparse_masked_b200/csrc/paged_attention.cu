@@ -12,20 +12,27 @@
 //    An item inside one run is finished there; one that is cut leaves fp32
 //    partial sums, which a second kernel joins in a fixed order (no atomics:
 //    equal calls give equal bits).  Lengths are device data and the grid does
-//    not depend on them, so a captured graph serves growing sequences.
+//    not depend on them, so a captured graph serves growing sequences.  Runs
+//    handed out as warps become free (fixed chunks, joined in order) were no
+//    better: 103 us against 99 for 64 sequences of 256 to 8192 keys.
 //  - Warps work alone: each looks its pages up, fills a ring of tiles of its
 //    own in shared memory (bf16: TMA, swizzled boxes; 4 bits: cp.async, whole
 //    code rows) and keeps its own running maximum and sums; the ring runs on
-//    into the next item, so the loads never pause at an item's end.
-//  - Few short items (a table of a few tiles per warp) take one CTA each
-//    instead, whose warps share the tiles and join their sums in shared memory.
+//    into the next item, so the loads never pause at an item's end.  (A ring
+//    shared by the warps needs two waits on one phase and a warp that fills
+//    it; it took 133 us.)
+//  - Few short items take one CTA each instead, whose warps share the tiles
+//    and join their sums in shared memory; many of a few tiles go whole to a
+//    warp.  Neither needs the second kernel.
 //  - Masks.  With mask vectors a plan kernel runs first: it turns each key's
-//    four boundaries into one bit per row, and lists the tiles that some row
-//    sees, so hidden tiles are neither read nor counted as work.
+//    boundaries into one bit per row, and a second one lists the tiles that
+//    some row sees, so hidden tiles are neither read nor counted as work.
+//    Items of one CTA turn the boundaries into bits themselves.
 //  - Products.  Tensor cores with the keys as the M side (mma m16n8k16): S^T =
 //    K Q^T and O^T = V^T P^T need only 8 row columns, where the usual
 //    orientation pads the rows to 16.  mma.sync and not tcgen05: rows are
-//    few, P never leaves registers, and the tensor pipe is far from the bound.
+//    few, P never leaves registers, and the tensor pipe is far from the bound
+//    (10 % busy in bf16, 18 % in 4 bits).
 //  - 4 bits.  A row's codes enter the products as integers, exact in bf16 (K:
 //    16 + code, which costs no subtraction, with -24 sum(q) as the sum's first
 //    value; V: code - 8); scale and minimum are applied to sums in fp32:
@@ -33,6 +40,16 @@
 //      o   = sum (p s)(c - 8) + sum p (m + 8 s)
 //    The contraction may run over the head's values in any order as long as
 //    both sides agree, so each thread takes whole 16-byte pieces of code rows.
+//    Codes as e4m3 bytes, which would need no conversion, lose: m16n8k32 in
+//    e4m3 issues every 21 clocks, m16n8k16 in bf16 every 8.5.
+//
+// Measured, heads of 128, 8 KV heads of 4 q-heads, one new token for each of 64 sequences of 256 to 8192 keys (262
+// thousand in all): bf16 99 us, 90 % of the measured copy bandwidth over the bytes that it cannot do
+// without; the rest is the chain lengths - pages - rows - tiles at the start, the merge, and SMs whose
+// bandwidth differs by 11 %.  In 4 bits 50 us, 44 %: the codes' conversion, 1400 instructions for 64 keys,
+// keeps half of the ALU pipe and of the issue slots busy with three warps a scheduler, which is as many as 168
+// registers allow.  A call of one tile takes 5.6 us: launch, the same chain, and code that is not in the
+// instruction cache.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -46,7 +63,10 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kMetaInts = 8;
-constexpr int kMinUnits = 2;  // units that a run holds at least (kItemCost of them may stand for an item)
+// Units that a run holds at least (kItemCost of them may stand for an item).  A long sequence with few visible
+// tiles wants short runs on every SM: 20 us with 2 for the window of two sequences of 64K keys, 26 with 6; 1 and
+// 2 are alike.
+constexpr int kMinUnits = 2;
 
 // ---------------------------------------------------------------------------
 // work: groups of items with the same number of tiles, and a CTA's run of units
@@ -91,7 +111,8 @@ struct Seqs {
 // Runs are made of units, or of whole items.  An item has a unit for each of
 // its tiles and kItemCost units before them, which stand for what an item
 // costs besides (rows of Q, pages, output): a run of many short items would
-// end late without them.
+// end late without them.  With 0, 2 and 4: 64 sequences of up to 8K keys 100.9, 98.9 and 99.3 us, in 4 bits 52.0, 50.1
+// and 52.4, 41 sequences of up to 6.7K keys 32.5, 30.6 and 30.8.
 constexpr int kItemCost = 2;
 struct Walk {
   int g, in, T;   // group, item in the group, tiles of the group's items
@@ -1268,9 +1289,11 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
 
 // ---------------------------------------------------------------------------
 // plan: row-visibility words and the class of every tile (one warp per tile),
-// then the list of visible tiles (one CTA per group).  A cluster of 8 CTAs per
-// group that does both in one launch took 30 us for one sequence of 128K keys:
-// 8 SMs do not have enough loads in flight for 2 MB of vectors.
+// then the list of visible tiles (one CTA per group); 3 us each.  A cluster of 8
+// CTAs per group that does both in one launch took 30 us for one sequence of
+// 128K keys: 8 SMs do not have enough loads in flight for 2 MB of vectors.
+// Lists made by every attention CTA for itself save 1 us with few groups, but
+// cost 2 where one group has 4096 tiles and 19 with 400 groups of one tile.
 // ---------------------------------------------------------------------------
 template <int KT>
 __global__ void __launch_bounds__(256) paged_plan_kernel(const __grid_constant__ PagedAttnParams p, PlanOut out) {
