@@ -1230,36 +1230,46 @@ __device__ __forceinline__ Joined join(const PagedAttnParams& p, int run, int fi
   return j;
 }
 
+constexpr int kMergeRuns = 16;  // runs of a CTA
+
 template <int D, int ROWS>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int workers) {
-  __shared__ int metas[8][kMetaInts];
   __shared__ float ms[8], ls[8];
   __shared__ float4 os[8][32];
   griddep_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y, v0 = blockIdx.x * 8;
-  if (tid < 8 * kMetaInts)
-    metas[tid / kMetaInts][tid % kMetaInts] = v0 + tid / kMetaInts < workers ? p.meta[v0 * kMetaInts + tid] : -1;
-  __syncthreads();
-  auto store = [&](const int* meta, const Joined& j) {
-    const int row = meta[2] + r, i = p.div_g(row), h = meta[1] * p.G + row - i * p.G, d4 = lane % (D / 4);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y, v0 = blockIdx.x * kMergeRuns;
+  // every warp reads what begins in the CTA's runs, a lane per run
+  int4 it = make_int4(-1, 0, 0, 0);  // sequence, KV head, first row, last run
+  int slot = 0;
+  if (lane < kMergeRuns && v0 + lane < workers) {
+    const int* meta = p.meta + (v0 + lane) * kMetaInts;
+    it = *reinterpret_cast<const int4*>(meta);
+    slot = meta[4];
+  }
+  const int mine = it.x < 0 || it.z + r >= p.Nq * p.G ? 0 : it.w - (v0 + lane) + 1;  // parts of the lane's item
+  auto store = [&](int x, const Joined& j) {
+    const int b = __shfl_sync(0xffffffffu, it.x, x), kvh = __shfl_sync(0xffffffffu, it.y, x);
+    const int row = __shfl_sync(0xffffffffu, it.z, x) + r, i = p.div_g(row), h = kvh * p.G + row - i * p.G;
+    const int d4 = lane % (D / 4);
     const float inv = j.m == -INFINITY ? 0.f : 1.f / j.l;
     if (lane >= D / 4) return;
-    *reinterpret_cast<uint2*>(p.o + (((int64_t)meta[0] * p.Nq + i) * p.Hq + h) * D + 4 * d4) =
+    *reinterpret_cast<uint2*>(p.o + (((int64_t)b * p.Nq + i) * p.Hq + h) * D + 4 * d4) =
         make_uint2(pack_bf16x2(j.o.x * inv, j.o.y * inv), pack_bf16x2(j.o.z * inv, j.o.w * inv));
     if (d4 == 0)
-      p.lse[((int64_t)meta[0] * p.Hq + h) * p.Nq + i] =
-          j.m == -INFINITY ? -INFINITY : fmaf(j.m, p.scale_log2, log2f(j.l)) * kLn2;
+      p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] = j.m == -INFINITY ? -INFINITY : fmaf(j.m, p.scale_log2, log2f(j.l)) * kLn2;
   };
-  auto parts_of = [&](int x) { return metas[x][0] < 0 || metas[x][2] + r >= p.Nq * p.G ? 0 : metas[x][3] - (v0 + x) + 1; };
-  {
-    const int parts = parts_of(warp);
-    if (parts > 0 && parts <= 16)
-      store(metas[warp], join<D, ROWS>(p, v0 + warp, metas[warp][4], parts, 0, 1, r));
-  }
-  for (int x = 0; x < 8; ++x) {
-    const int parts = parts_of(x);
-    if (parts <= 16) continue;
-    Joined j = join<D, ROWS>(p, v0 + x, metas[x][4], parts, warp, 8, r);
+  auto joined = [&](int x, int k0, int step) {
+    return join<D, ROWS>(p, v0 + x, __shfl_sync(0xffffffffu, slot, x), __shfl_sync(0xffffffffu, mine, x), k0, step, r);
+  };
+  int at = 0;
+  for (uint32_t few = __ballot_sync(0xffffffffu, mine > 0 && mine <= 16); few; few &= few - 1)
+    if ((at++ & 7) == warp) {
+      const int x = __ffs(few) - 1;
+      store(x, joined(x, 0, 1));
+    }
+  for (uint32_t many = __ballot_sync(0xffffffffu, mine > 16); many; many &= many - 1) {
+    const int x = __ffs(many) - 1;
+    const Joined j = joined(x, warp, 8);
     __syncthreads();
     if (lane == 0) {
       ms[warp] = j.m;
@@ -1283,7 +1293,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
       all.o.z = fmaf(o.z, f, all.o.z);
       all.o.w = fmaf(o.w, f, all.o.w);
     }
-    store(metas[x], all);
+    store(x, all);
   }
 }
 
@@ -1384,7 +1394,7 @@ static cudaError_t launch_variant(const PagedAttnParams& p, const CUtensorMap& t
   }
   if (e != cudaSuccess || p.mode != kPagedSplit) return e;
   const int workers = grid * C::kWarps;
-  return launch_after(paged_merge_kernel<D, C::kRows>, dim3((workers + 7) / 8, std::min(C::kRows, p.Nq * p.G)), dim3(256),
+  return launch_after(paged_merge_kernel<D, C::kRows>, dim3((workers + kMergeRuns - 1) / kMergeRuns, std::min(C::kRows, p.Nq * p.G)), dim3(256),
                       0, st, p, workers);
 }
 
