@@ -105,18 +105,25 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
   const bool wide = pg.bits == 16 && !masked && blocks(32) * pg.B * pg.Hkv * tiles >= 24 * 4 * kSms;  // 24 tiles a warp
   L.rows = R <= 8 ? 8 : R <= 16 || !wide ? 16 : 32;
   // Whole items where cutting has nothing to give, and no second kernel.  One per CTA if the table bounds them to
-  // four tiles a warp and the device takes them all at once, in the smallest blocks of rows for which it
-  // does (4 sequences of 103 keys and 32 rows: 10.7 us in blocks of 32, 6.8 in blocks of 8); masks are then read with
-  // the tiles, without a plan.  One after another per warp if the table bounds them to eight tiles (20
-  // sequences of 110 keys: 10 us, 16 with four waves of CTAs).  Else cut, unless two waves of CTAs take them
-  // (30 sequences of 1079 keys with masks, 4 bits: 22 us, cut 32; 21 of 385 keys without: 11.0 and 11.9).
+  // four tiles a warp and the device takes them all at once, in the smallest blocks of rows for which it does (4
+  // sequences of 103 keys and 32 rows: 10.7 us in blocks of 32, 6.8 in blocks of 8); masks are then read with the
+  // tiles, without a plan, and hidden tiles with them.  8 KV heads of 4 sequences of 700 keys: 9.3 us, cut 10.8, with
+  // masks 12.0 and 14.1.  In 4 bits a round of tiles takes 3.4 us at d = 128, and an item that leaves SMs idle for
+  // more than 1.25 rounds (2 with masks, whose plan counts too) is better cut: 32 items of 3000 keys 20 us, cut 14, but
+  // 144 of 2000 keys 16.1 and 18.1.  One after another per warp if the table bounds them to eight tiles (20 sequences of 110 keys: 10 us, 16
+  // with four waves of CTAs).  Else cut, unless two waves of CTAs take items of some twelve tiles (29 sequences
+  // of 619 keys with masks in 4 bits: 17.2 us, cut 19.6; 36 of 1300 keys 24 and 20).
   L.mode = tiles <= 8 ? kPagedWhole : kPagedSplit;
   for (int waves = 1; waves <= (tiles <= 8 ? 1 : 2) && L.mode != kPagedCoop; ++waves)
-    for (int rows = 8; rows <= (pg.bits == 16 ? 32 : 16) && L.mode != kPagedCoop; rows *= 2)
-      if (blocks(rows) * pg.B * pg.Hkv <= waves * kSms && tiles <= 4 * paged_warps(pg.d, pg.bits, rows)) {
-        L.mode = kPagedCoop;
-        L.rows = rows;
-      }
+    for (int rows = 8; rows <= (pg.bits == 16 ? 32 : 16) && L.mode != kPagedCoop; rows *= 2) {
+      const int warps = paged_warps(pg.d, pg.bits, rows);
+      const int64_t items = blocks(rows) * pg.B * pg.Hkv;
+      const int64_t most = waves == 1 ? 4 * warps : pg.bits == 16 ? 2 * warps : warps;
+      if (items > waves * kSms || tiles > most) continue;
+      if (waves == 1 && pg.bits == 4 && 4 * (kSms - items) * tiles * pg.d > (masked ? 8 : 5) * 128 * kSms * warps) continue;
+      L.mode = kPagedCoop;
+      L.rows = rows;
+    }
   L.n_rb = (int)blocks(L.rows);
   const int warps = paged_warps(pg.d, pg.bits, L.rows);
   L.plan = masked && tiles > 0 && L.mode != kPagedCoop;
