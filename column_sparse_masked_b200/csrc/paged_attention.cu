@@ -46,7 +46,7 @@
 // Measured, heads of 128, 8 KV heads of 4 q-heads, one new token for each of 64 sequences of 256 to 8192 keys (262
 // thousand in all): bf16 99 us, 90 % of the measured copy bandwidth over the bytes that it cannot do
 // without; the rest is the chain lengths - pages - rows - tiles at the start, the merge, and SMs whose
-// bandwidth differs by 11 %.  In 4 bits 50 us, 44 %: the codes' conversion, 1400 instructions for 64 keys,
+// bandwidth differs by 11 %.  In 4 bits 48.7 us, 45 %: the codes' conversion, 1400 instructions for 64 keys,
 // keeps half of the ALU pipe and of the issue slots busy with three warps a scheduler, which is as many as 168
 // registers allow.  A call of one tile takes 5.6 us: launch, the same chain, and code that is not in the
 // instruction cache.
@@ -1168,7 +1168,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
 // joining the parts of cut items, in the order of their runs: a warp per item
 // and row where the parts are few, the CTA's 8 warps together where they are
 // many.  Latency is all it costs: the parts' values are asked for before their
-// weights are known.
+// weights are known, and of the items that begin in 16 runs each warp takes
+// its own without a barrier (with 8 runs a CTA, a warp for each, 9 sequences
+// of 32 rows took 26.6 us and now 20.9; with 32 runs 64 sequences take 102 us and
+// 99).
 // ---------------------------------------------------------------------------
 struct Joined {
   float m, l;
