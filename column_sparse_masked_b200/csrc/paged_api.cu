@@ -109,9 +109,9 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
   // sequences of 103 keys and 32 rows: 10.7 us in blocks of 32, 6.8 in blocks of 8); masks are then read with the
   // tiles, without a plan, and hidden tiles with them.  8 KV heads of 4 sequences of 700 keys: 9.3 us, cut 10.8, with
   // masks 12.0 and 14.1.  In 4 bits a round of tiles takes 3.4 us at d = 128, and an item that leaves SMs idle for
-  // more than 1.25 rounds (2 with masks, whose plan counts too) is better cut: 32 items of 3000 keys 20 us, cut 14, but
-  // 144 of 2000 keys 16.1 and 18.1.  One after another per warp if the table bounds them to eight tiles (20 sequences of 110 keys: 10 us, 16
-  // with four waves of CTAs).  Else cut, unless two waves of CTAs take items of some twelve tiles (29 sequences
+  // more than 1.25 rounds (2 with masks, whose plan counts too) is better cut: 32 items of 3000 keys 20 us, cut 14,
+  // but 144 of 2000 keys 16.1 and 18.1.  One after another per warp if the table bounds them to eight tiles (20
+  // sequences of 110 keys: 10 us, 16 with four waves of CTAs).  Else cut, unless two waves of CTAs take items of some twelve tiles (29 sequences
   // of 619 keys with masks in 4 bits: 17.2 us, cut 19.6; 36 of 1300 keys 24 and 20).
   L.mode = tiles <= 8 ? kPagedWhole : kPagedSplit;
   for (int waves = 1; waves <= (tiles <= 8 ? 1 : 2) && L.mode != kPagedCoop; ++waves)

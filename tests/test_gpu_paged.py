@@ -308,6 +308,18 @@ def test_attention_more_rows_than_a_block(bits, Hm, shape):
 
 
 @pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("G", [3, 5, 12, 40])
+@pytest.mark.parametrize("lens,width", [([150, 33], None), ([60, 64] * 40, None), ([700, 90], 60)])
+def test_attention_mask_heads_that_do_not_divide_a_block(bits, G, lens, width):
+    """A mask head for each q-head, with groups of heads that end inside a block of rows: one item per CTA, per warp,
+    and cut."""
+    Nq = 7 if len(lens) == 2 else 2
+    cache = Cache(31, lens, 2, 64, 64, bits, width=width).cuda()
+    vec = masks("random", len(lens), 2 * G, max(lens), 16, Nq)
+    check_attention(case_q(len(lens), Nq, 2 * G, 64), cache, lens, vec)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("Hm,width", [(0, None), (1, None), (2, None), (0, 48), (1, 48), (2, 48)])
 def test_attention_more_sequences_than_shared_memory_holds(bits, Hm, width):
     rng = np.random.default_rng(6)
