@@ -1083,8 +1083,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
     if (at < p.q_bytes) prefetch_l2(reinterpret_cast<const char*>(p.q) + at);
     if (at < p.table_bytes) prefetch_l2(reinterpret_cast<const char*>(p.pg.table) + at);
   }
-  griddep_wait();
-  griddep_launch_dependents();
   const Seqs sq{sm.seq, sm.counts, p.pg.B <= kSeqCache, p.n_groups <= kSeqCache};
   if (sq.has_seq)
     for (int b = tid; b < p.pg.B; b += C::kThreads) {
@@ -1092,6 +1090,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
       sm.seq[b] = q;
       if (!p.counts && sq.has_tiles && !p.per_head) sm.counts[b] = (key_bound(p, q) + C::kKT - 1) / C::kKT;
     }
+  griddep_wait();  // the plan; what is read above are the call's inputs, which were there before the plan began
+  griddep_launch_dependents();
   if (p.counts && sq.has_tiles)
     for (int g = tid; g < p.n_groups; g += C::kThreads) sm.counts[g] = p.counts[g];
   __syncthreads();
