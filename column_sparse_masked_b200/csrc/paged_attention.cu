@@ -44,9 +44,9 @@
 //    e4m3 issues every 21 clocks, m16n8k16 in bf16 every 8.5.
 //
 // Measured, heads of 128, 8 KV heads of 4 q-heads, one new token for each of 64 sequences of 256 to 8192 keys (262
-// thousand in all): bf16 99 us, 90 % of the measured copy bandwidth over the bytes that it cannot do
+// thousand in all): bf16 98.6 us, 90 % of the measured copy bandwidth over the bytes that it cannot do
 // without; the rest is the chain lengths - pages - rows - tiles at the start, the merge, and SMs whose
-// bandwidth differs by 11 %.  In 4 bits 48.7 us, 45 %: the codes' conversion, 1400 instructions for 64 keys,
+// bandwidth differs by 11 %.  In 4 bits 48.2 us, 46 %: the codes' conversion, 1400 instructions for 64 keys,
 // keeps half of the ALU pipe and of the issue slots busy with three warps a scheduler, which is as many as 168
 // registers allow.  A call of one tile takes 5.6 us: launch, the same chain, and code that is not in the
 // instruction cache.
@@ -1168,10 +1168,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kThreads, 1)
 // joining the parts of cut items, in the order of their runs: a warp per item
 // and row where the parts are few, the CTA's 8 warps together where they are
 // many.  Latency is all it costs: the parts' values are asked for before their
-// weights are known, and of the items that begin in 16 runs each warp takes
-// its own without a barrier (with 8 runs a CTA, a warp for each, 9 sequences
-// of 32 rows took 26.6 us and now 20.9; with 32 runs 64 sequences take 102 us and
-// 99).
+// weights are known, and of the items that begin in a CTA's runs each warp takes
+// its own without a barrier (with one warp for each run and barriers, 9 sequences
+// of 32 rows took 26.6 us, now 20.9).
 // ---------------------------------------------------------------------------
 struct Joined {
   float m, l;
@@ -1233,18 +1232,17 @@ __device__ __forceinline__ Joined join(const PagedAttnParams& p, int run, int fi
   return j;
 }
 
-constexpr int kMergeRuns = 16;  // runs of a CTA
-
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int workers) {
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int workers,
+                                                          int runs) {
   __shared__ float ms[8], ls[8];
   __shared__ float4 os[8][32];
   griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y, v0 = blockIdx.x * kMergeRuns;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y, v0 = blockIdx.x * runs;
   // every warp reads what begins in the CTA's runs, a lane per run
   int4 it = make_int4(-1, 0, 0, 0);  // sequence, KV head, first row, last run
   int slot = 0;
-  if (lane < kMergeRuns && v0 + lane < workers) {
+  if (lane < runs && v0 + lane < workers) {
     const int* meta = p.meta + (v0 + lane) * kMetaInts;
     it = *reinterpret_cast<const int4*>(meta);
     slot = meta[4];
@@ -1396,9 +1394,12 @@ static cudaError_t launch_variant(const PagedAttnParams& p, const CUtensorMap& t
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || p.mode != kPagedSplit) return e;
-  const int workers = grid * C::kWarps;
-  return launch_after(paged_merge_kernel<D, C::kRows>, dim3((workers + kMergeRuns - 1) / kMergeRuns, std::min(C::kRows, p.Nq * p.G)), dim3(256),
-                      0, st, p, workers);
+  // Runs of a CTA: 8 while all CTAs fit on the device at once (three an SM), else 16.  64 sequences of 4 rows: 98.0 us
+  // with 8, 99.7 with 16; 9 sequences of 32 rows 22.5 and 20.9.
+  const int workers = grid * C::kWarps, rows = std::min(C::kRows, p.Nq * p.G);
+  const int runs = (workers + 7) / 8 * rows <= 3 * 148 ? 8 : 16;
+  return launch_after(paged_merge_kernel<D, C::kRows>, dim3((workers + runs - 1) / runs, rows), dim3(256), 0, st, p, workers,
+                      runs);
 }
 
 template <int D, int BITS>
