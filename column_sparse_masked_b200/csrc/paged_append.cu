@@ -71,17 +71,22 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float (&c)[8], cons
 }
 
 // The code of x in a row with minimum lo, as a float: the integer nearest to
-// (x - lo) / scale, ties to even.  The quotient in fp32 only proposes; the
-// decision is |x - lo - k scale| against half the scale, which fp32 gives
-// without error (k scale has 12 bits, and the difference x - lo comes with its
-// rounding error, Knuth's sum).  Ties are common, since values and scales lie on
-// the same few binary places: one value in some 300 of normal data.
-__device__ __forceinline__ float code_of(float x, float lo, float scale, float inv, float half, float below_half) {
+// (x - lo) / scale, ties to even.  The quotient in fp32 only proposes an integer
+// k; the decision is whether |x - lo - k scale| exceeds half the scale.  x - lo is
+// diff + err without error (Knuth's sum), r = diff - k scale is exact (k scale has
+// 12 bits), and so is |r| - half wherever err, at most 2^-20 of the scale, can decide.
+// err is added to that last, small difference: fp32 addition rounds no sum across
+// zero, whereas r + err can round onto the middle of two codes.  Ties are
+// common, since values and scales lie on the same few binary places: one value in
+// some 300 of normal data.
+__device__ __forceinline__ float code_of(float x, float lo, float scale, float inv, float half) {
   const float diff = x - lo, z = diff - x, err = (x - (diff - z)) + (-lo - z);
   const float m = fmaf(diff, inv, 12582912.f), k = m - 12582912.f;  // to an integer, which is in m's low bits
-  const float e = fmaf(-k, scale, diff) + err;
-  const float limit = (__float_as_uint(m) & 1u) ? below_half : half;  // an odd code gives way at the middle
-  return fabsf(e) > limit ? k + copysignf(1.f, e) : k;
+  const float r = fmaf(-k, scale, diff);
+  const float over = (fabsf(r) - half) + __uint_as_float(__float_as_uint(err) ^ (__float_as_uint(r) & 0x80000000u));
+  // an odd code gives way at the middle: over >= 0, written as over > the least number below 0
+  const float limit = __uint_as_float((__float_as_uint(m) & 1u) ? 0x80000001u : 0u);
+  return over > limit ? k + copysignf(1.f, r) : k;
 }
 
 // Lower of two bf16 pairs, NaN if either is.
@@ -214,12 +219,12 @@ __global__ void __launch_bounds__(128, BITS == 4 ? 8 : 1) paged_append_kernel(Ap
 #pragma unroll
         for (int j = 0; j < 16; ++j) x[j] *= 0x1p64f;
       }
-      const float inv = 1.f / scale, half = 0.5f * scale, below_half = __uint_as_float(__float_as_uint(half) - 1u);
+      const float inv = 1.f / scale, half = 0.5f * scale;
       // codes are put together four at a time as a sum of code * 16^j, exact in fp32
       float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        float k = code_of(x[j], lo, scale, inv, half, below_half);
+        float k = code_of(x[j], lo, scale, inv, half);
         if (tiny) k = fminf(k, 15.f);  // the scale of so small a spread may be rounded down by a half
         part[j >> 2] = fmaf(k, (float)(1 << (4 * (j & 3))), part[j >> 2]);
       }

@@ -1,0 +1,73 @@
+"""Paged key/value cache on the GPU, at values, outputs and calls that tests/test_gpu_paged.py does not reach: codes
+whose exact quotient lies beside the middle of two codes by less than fp32 sees."""
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+import column_sparse_masked_b200 as fm
+
+import _paged as ref
+from _paged import Cache, bf16, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    fm.get_status()
+    yield
+    assert fm.get_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# append, 4 bits: the code decision
+# ---------------------------------------------------------------------------
+def nearest_code(x, lo, scale):
+    """The integer nearest to (x - lo) / scale, ties to even, in rational arithmetic."""
+    return min(max(round((Fraction(x) - Fraction(lo)) / Fraction(scale)), 0), 15)  # Fraction: ties to even
+
+
+def rows_beside_the_middle(d):
+    """Rows of bf16 values with quotients on the middle of two codes but for a term that a sum in fp32 loses: a
+    minimum of (k + 1/2) steps and values near 0, or a minimum near 0 and values of (k + 1/2) steps."""
+    rows = []
+    for a in (-60, -3, 0, 1, 40):
+        step = 2.0 ** a
+        tiny = [0.0] + [s * m * step * 2.0 ** -e for e in (8, 20, 23, 24, 25, 26, 30, 33, 60) for s in (1, -1)
+                        for m in (1.0, 1.5)]
+        for k in range(16):  # 0 lies k + 1/2 (or k) steps above the minimum
+            for part in (0.5, 0.0):
+                lo = -(k + part) * step
+                x = [lo, lo + 15 * step] + tiny
+                rows.append(x + [0.0] * (d - len(x)))
+        odd = [(k + 0.5) * step for k in range(15)]
+        for t in tiny:
+            x = [t if t < 0 else min(t, 0.25 * step), 15 * step] + odd + [k * step for k in range(1, 15)]
+            rows.append(x + [step] * (d - len(x)))
+    return bf16(np.array(rows))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_codes_beside_the_middle_of_two(d):
+    """Every code is the nearest one for the row's stored scale and minimum, ties to even, in rational arithmetic."""
+    x = rows_beside_the_middle(d)
+    x = np.concatenate([x, x[:, ::-1]])
+    n = len(x)
+    cache = Cache(71, [n], 1, d, 64, 4).cuda()
+    t = torch.from_numpy(x).bfloat16().reshape(1, n, 1, d).cuda()
+    assert np.array_equal(f64(t).reshape(n, d), x)
+    fm.paged_append(t, t, cache.k, cache.v, cache.table, i32([0]), **cache.kw)
+    page = cache.table[0].cpu().numpy()[np.arange(n) // 64]
+    for codes, scales in ((cache.k, cache.ks), (cache.v, cache.vs)):
+        c, s = codes.cpu().numpy()[page, 0, np.arange(n) % 64], f64(scales)[page, 0, np.arange(n) % 64]
+        got = np.stack([c & 15, c >> 4], -1).reshape(n, d)
+        _, scale, lo = ref.quantise(x)
+        assert np.array_equal(s, np.stack([scale, lo], -1))
+        want = np.array([[nearest_code(y, lo[i], scale[i]) for y in x[i]] for i in range(n)])
+        assert np.array_equal(got, want)
