@@ -37,6 +37,7 @@ struct GatherParams {
   const int32_t* lens;
   int N;
   __nv_bfloat16 *k, *v;
+  int wide;  // k and v are 32-byte aligned
 };
 
 // Division of numbers below 2^31 by a constant of the call: x / d = (x * m) >> 32 >> s with m = ceil(2^(32 + s) / d),

@@ -312,7 +312,7 @@ int flashmask_paged_gather(const flashmask_pages* pages, const int32_t* lens, in
   if ((int64_t)pages->B * N > INT_MAX / pages->Hkv) return FLASHMASK_ERR_UNSUPPORTED;
   if ((int64_t)pages->B * N == 0) return FLASHMASK_OK;
   if (!lens || !k || !v) return FLASHMASK_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) return FLASHMASK_ERR_ALIGN;
+  if (!aligned16(k) || !aligned16(v)) return FLASHMASK_ERR_ALIGN;
   DeviceInfo di;
   FM_TRY(current_device(&di));
   GatherParams p{};
@@ -321,6 +321,7 @@ int flashmask_paged_gather(const flashmask_pages* pages, const int32_t* lens, in
   p.N = N;
   p.k = static_cast<__nv_bfloat16*>(k);
   p.v = static_cast<__nv_bfloat16*>(v);
+  p.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
   FM_CUDA(launch_paged_gather(p, static_cast<cudaStream_t>(stream)));
   return FLASHMASK_OK;
 }

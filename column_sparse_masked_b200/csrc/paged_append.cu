@@ -259,7 +259,7 @@ __device__ __forceinline__ void values8(uint32_t x, __nv_bfloat162 scale, __nv_b
   out[3] = __byte_perm(v[2], v[3], 0x7632);
 }
 
-// One thread writes 16 values of k and of v (32-byte stores, whole rows by
+// One thread writes 16 values of k and of v (32-byte stores where the outputs allow, whole rows by
 // D/16 lanes): neighbouring lanes take neighbouring heads of one token, as the
 // output has them.
 template <int D, int BITS>
@@ -296,8 +296,16 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(GatherParams p, int64
       }
     }
   }
-  st_global_v8_na(p.k + out_row * D + 16 * e, wk);
-  st_global_v8_na(p.v + out_row * D + 16 * e, wv);
+  __nv_bfloat16 *ok = p.k + out_row * D + 16 * e, *ov = p.v + out_row * D + 16 * e;
+  if (p.wide) {
+    st_global_v8_na(ok, wk);
+    st_global_v8_na(ov, wv);
+  } else {  // outputs inside a buffer, 16-byte aligned as everything else
+    st_global_v4_na(ok, wk[0], wk[1], wk[2], wk[3]);
+    st_global_v4_na(ok + 8, wk[4], wk[5], wk[6], wk[7]);
+    st_global_v4_na(ov, wv[0], wv[1], wv[2], wv[3]);
+    st_global_v4_na(ov + 8, wv[4], wv[5], wv[6], wv[7]);
+  }
 }
 
 }  // namespace

@@ -1,5 +1,6 @@
 """Paged key/value cache on the GPU, at values, outputs and calls that tests/test_gpu_paged.py does not reach: codes
-whose exact quotient lies beside the middle of two codes by less than fp32 sees."""
+whose exact quotient lies beside the middle of two codes by less than fp32 sees, and outputs inside the caller's
+buffers."""
 from fractions import Fraction
 
 import numpy as np
@@ -71,3 +72,32 @@ def test_codes_beside_the_middle_of_two(d):
         assert np.array_equal(s, np.stack([scale, lo], -1))
         want = np.array([[nearest_code(y, lo[i], scale[i]) for y in x[i]] for i in range(n)])
         assert np.array_equal(got, want)
+
+
+# ---------------------------------------------------------------------------
+# gather: outputs inside the caller's buffers
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at_k,at_v", [(8, 16), (16, 8), (8, 24), (0, 0)])
+def test_gather_into_16_byte_aligned_outputs(bits, d, at_k, at_v):
+    """Outputs anywhere in a buffer, as long as they are 16-byte aligned; nothing beside them is written."""
+    lens, N, Hkv = [37, 0, 64], 50, 3
+    cache = Cache(72, lens, Hkv, d, 16, bits).cuda()
+    want = fm.paged_gather(cache.k, cache.v, cache.table, i32(lens), N, **cache.kw)
+    size = want[0].numel()
+    buffers = [torch.full((size + 48,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    out = tuple(x[a:a + size].view(want[0].shape) for x, a in zip(buffers, (at_k, at_v)))
+    got = fm.paged_gather(cache.k, cache.v, cache.table, i32(lens), N, out=out, **cache.kw)
+    assert got[0] is out[0] and got[1] is out[1]
+    for x, a, w in zip(buffers, (at_k, at_v), want):
+        assert torch.equal(x[a:a + size].view(w.shape), w)
+        assert (x[:a] == 7).all() and (x[a + size:] == 7).all()
+
+
+def test_gather_refuses_outputs_off_the_16_byte_grid():
+    cache = Cache(72, [20], 1, 64, 16, 16).cuda()
+    x = torch.zeros(2, 20 * 64 + 8, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(fm.FlashMaskError, match="align"):
+        fm.paged_gather(cache.k, cache.v, cache.table, i32([20]), 20,
+                        out=(x[0, 4:4 + 20 * 64].view(1, 20, 1, 64), x[1, :20 * 64].view(1, 20, 1, 64)))
