@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(128, BITS == 4 ? 8 : 1) paged_append_kernel(Ap
         if (turns) rotate<false>(x, c, s, p.interleaved);
         pack_chunks(x, w);
       }
-      store_chunks(ob + r * D, a, bo, w);
+      store_chunks(ob + (int64_t)r * D, a, bo, w);
     }
   }
   if (!store_ok) return;

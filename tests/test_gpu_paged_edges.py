@@ -101,3 +101,21 @@ def test_gather_refuses_outputs_off_the_16_byte_grid():
     with pytest.raises(fm.FlashMaskError, match="align"):
         fm.paged_gather(cache.k, cache.v, cache.table, i32([20]), 20,
                         out=(x[0, 4:4 + 20 * 64].view(1, 20, 1, 64), x[1, :20 * 64].view(1, 20, 1, 64)))
+
+
+# ---------------------------------------------------------------------------
+# append: offsets that pass 32 bits
+# ---------------------------------------------------------------------------
+def test_append_q_rows_whose_offsets_pass_31_bits():
+    """A row of more than 2^24 q-heads of 128: values beyond the 2^31st of q_out are where they belong, and those in
+    front of the buffer's start (where a wrapped offset would point) are left alone."""
+    Hq, d = (1 << 24) + 5, 128
+    cache = Cache(73, [1], 1, d, 16, 16).cuda()
+    row = torch.randn(1, 1, 1, d, device="cuda").bfloat16()
+    lead = 1 << 16
+    buf = torch.full((lead + Hq * d,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[lead:].view(1, 1, Hq, d)
+    fm.paged_append(row, row, cache.k, cache.v, cache.table, i32([0]), q=row.expand(1, 1, Hq, d), q_out=out)
+    assert (buf[:lead] == 7).all()
+    for a in range(0, Hq, 1 << 22):
+        assert torch.equal(out[0, 0, a:a + (1 << 22)], row[0, 0].expand(min(1 << 22, Hq - a), d)), a
