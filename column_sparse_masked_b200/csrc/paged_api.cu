@@ -70,8 +70,8 @@ int check_paged_rows(const flashmask_pages* pg, const flashmask_paged_rows* r) {
   if (r->lts || r->uts) {
     if (r->Nm < 0 || (r->Hm != 1 && r->Hm != r->Hq)) return FLASHMASK_ERR_INVALID_ARG;
   }
-  // work items are numbered in 32 bits
-  if ((int64_t)pg->B * r->Nq * r->Hq > INT_MAX / 4) return FLASHMASK_ERR_UNSUPPORTED;
+  // work items are numbered in 32 bits (by division: the products may pass 64)
+  if ((int64_t)pg->B * r->Nq > INT_MAX / 4 / r->Hq) return FLASHMASK_ERR_UNSUPPORTED;
   const int64_t units = ((int64_t)pg->table_width * pg->page_size + 31) / 32 + 2;
   const int64_t blocks = ((int64_t)r->Nq * (r->Hq / pg->Hkv) + 7) / 8;
   if (blocks * pg->Hkv * pg->B > INT_MAX / 2 / units) return FLASHMASK_ERR_UNSUPPORTED;
@@ -178,8 +178,8 @@ int flashmask_paged_append(const flashmask_pages* pages, const flashmask_append*
   if (t.N < 0 || t.table_len < 0 || (t.interleaved != 0 && t.interleaved != 1)) return FLASHMASK_ERR_INVALID_ARG;
   if (t.q && t.Hq <= 0) return FLASHMASK_ERR_INVALID_ARG;
   if (t.rot < 0 || t.rot > pages->d || t.rot % 16 != 0) return FLASHMASK_ERR_UNSUPPORTED;
-  const int64_t rows = (int64_t)pages->B * t.N * ((t.q ? t.Hq : 0) + 2 * (int64_t)pages->Hkv);
-  if (rows > INT_MAX) return FLASHMASK_ERR_UNSUPPORTED;
+  // rows are numbered in 32 bits (by division: the product may pass 64)
+  if ((int64_t)pages->B * t.N > INT_MAX / ((t.q ? t.Hq : 0) + 2 * (int64_t)pages->Hkv)) return FLASHMASK_ERR_UNSUPPORTED;
   if ((int64_t)pages->B * t.N == 0) return FLASHMASK_OK;
   if (!t.start) return FLASHMASK_ERR_INVALID_ARG;
   if (t.rot > 0 && (!t.cos || !t.sin)) return FLASHMASK_ERR_INVALID_ARG;

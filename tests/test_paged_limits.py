@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from test_paged_checks import ALIGN, c_pages, library  # noqa: F401 (the fixture builds the library)
+from test_paged_checks import ALIGN, UNSUPPORTED, c_append, c_pages, c_rows, library  # noqa: F401 (the fixture builds the library)
 
 _P = ctypes.c_void_p
 
@@ -12,3 +12,13 @@ _P = ctypes.c_void_p
 @pytest.mark.parametrize("k,v", [(4104, 4096), (4096, 4104), (4098, 4112), (4120, 4120)])
 def test_c_gather_outputs_are_16_byte_aligned(library, k, v):  # noqa: F811
     assert library.flashmask_paged_gather(ctypes.byref(c_pages()), _P(4096), 5, _P(k), _P(v), None) == ALIGN
+
+
+def test_c_size_products_do_not_wrap(library):  # noqa: F811
+    """Sizes whose product passes 64 bits are refused like those that pass 32: 2^30 x 2^30 tokens of 16 rows."""
+    pg = c_pages(B=1 << 30, Hkv=4, num_pages=1)
+    assert library.flashmask_paged_append(ctypes.byref(pg), ctypes.byref(c_append(N=1 << 30, q=4096, q_out=4096, Hq=8)),
+                                          None) == UNSUPPORTED
+    r = c_rows(Nq=1 << 30, Hq=16)
+    assert library.flashmask_paged_attention_workspace_size(ctypes.byref(pg), ctypes.byref(r)) == 0
+    assert library.flashmask_paged_attention(ctypes.byref(pg), ctypes.byref(r), _P(4096), 1 << 30, None) == UNSUPPORTED
