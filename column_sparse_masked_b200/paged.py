@@ -219,7 +219,7 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     contiguous q itself), or None without q."""
     r = (_calls or _load()).append(k, v, k_pages, v_pages, block_table, start, counts, q, cos, sin, positions, interleaved,
                                    k_scales, v_scales, q_out)
-    if r is None or r.__class__ is torch.Tensor:
+    if r is None or isinstance(r, torch.Tensor):
         return r
     _fail(r, "flashmask_paged_append", _explain_append, k, v, k_pages, v_pages, block_table, start, counts, q, cos, sin,
           positions, k_scales, v_scales, q_out)

@@ -3,6 +3,7 @@ tests/test_paged_checks.py."""
 import ctypes
 
 import pytest
+import torch
 
 from test_paged_checks import ALIGN, UNSUPPORTED, c_append, c_pages, c_rows, library  # noqa: F401 (the fixture builds the library)
 
@@ -22,3 +23,17 @@ def test_c_size_products_do_not_wrap(library):  # noqa: F811
     r = c_rows(Nq=1 << 30, Hq=16)
     assert library.flashmask_paged_attention_workspace_size(ctypes.byref(pg), ctypes.byref(r)) == 0
     assert library.flashmask_paged_attention(ctypes.byref(pg), ctypes.byref(r), _P(4096), 1 << 30, None) == UNSUPPORTED
+
+
+def test_append_returns_a_q_out_of_any_tensor_class(monkeypatch):
+    """q_out comes back also where it is a Parameter (the call had run, and an error was raised for it)."""
+    from column_sparse_masked_b200 import paged
+
+    class Calls:
+        @staticmethod
+        def append(*a):
+            return a[-1]
+
+    monkeypatch.setattr(paged, "_calls", Calls)
+    out = torch.nn.Parameter(torch.zeros(2), requires_grad=False)
+    assert paged.paged_append(*[None] * 6, q_out=out) is out
