@@ -179,6 +179,8 @@ def _explain_attention(q, k_pages, v_pages, block_table, lens, lts, lte, uts, ut
         if ref.shape[1] not in (1, Hq):
             raise ValueError(f"mask vectors have {ref.shape[1]} heads, expected 1 or {Hq}")
     _strides("q", q)
+    if workspace is not None and not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     if o is not None or lse is not None:
         _is("o", o, _BF16, (B, Nq, Hq, d))
         _is("lse", lse, _F32, (B, Hq, Nq))
@@ -194,6 +196,8 @@ def _explain_gather(k_pages, v_pages, block_table, lens, N, k_scales, v_scales, 
         raise TypeError("N must be an integer")
     if N < 0:
         raise ValueError("N must not be negative")
+    if N >= 1 << 31:
+        raise ValueError("N must fit 32 bits")
     B, Hkv, d, dev = _pages(k_pages, v_pages, k_scales, v_scales, block_table)
     _is("lens", lens, _I32, (B,))
     if k is not None or v is not None:

@@ -5,7 +5,8 @@ import ctypes
 import pytest
 import torch
 
-from test_paged_checks import ALIGN, UNSUPPORTED, c_append, c_pages, c_rows, library  # noqa: F401 (the fixture builds the library)
+from test_paged_checks import (ALIGN, UNSUPPORTED, args, attend, c_append, c_pages, c_rows, gather,  # noqa: F401
+                               library)  # (the fixture builds the library)
 
 _P = ctypes.c_void_p
 
@@ -37,3 +38,15 @@ def test_append_returns_a_q_out_of_any_tensor_class(monkeypatch):
     monkeypatch.setattr(paged, "_calls", Calls)
     out = torch.nn.Parameter(torch.zeros(2), requires_grad=False)
     assert paged.paged_append(*[None] * 6, q_out=out) is out
+
+
+@pytest.mark.parametrize("workspace", [4096, "x", [torch.zeros(9)]])
+def test_a_workspace_that_is_no_tensor_is_named(workspace):
+    with pytest.raises(TypeError, match="workspace must be a torch.Tensor"):
+        attend(args(), workspace=workspace)
+
+
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 40])
+def test_gather_of_more_positions_than_32_bits_is_named(n):
+    with pytest.raises(ValueError, match="N must"):
+        gather(args(), n=n)
