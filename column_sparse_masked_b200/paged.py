@@ -23,7 +23,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._binding import FlashMaskError, lib_path, load_library
+from ._binding import FlashMaskError, load_library
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 _calls = None
@@ -32,12 +32,12 @@ _calls = None
 def _load():
     """The compiled marshalling of these calls (_paged_binding.so), bound to the library in use."""
     global _calls
-    load_library()
+    lib = load_library()
     try:
         from . import _paged_binding
     except ImportError as e:
         raise RuntimeError("_paged_binding.so is missing: build it with `python column_sparse_masked_b200/build.py`") from e
-    _paged_binding.bind(lib_path())
+    _paged_binding.bind(lib._name)
     _calls = _paged_binding
     return _calls
 

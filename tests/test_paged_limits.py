@@ -1,9 +1,12 @@
 """Paged-cache calls that are refused before any launch, and the errors that name them (CPU only), beside those of
 tests/test_paged_checks.py."""
 import ctypes
+import sys
 
 import pytest
 import torch
+
+import column_sparse_masked_b200 as fm
 
 from test_paged_checks import (ALIGN, UNSUPPORTED, args, attend, c_append, c_pages, c_rows, gather,  # noqa: F401
                                library)  # (the fixture builds the library)
@@ -50,3 +53,24 @@ def test_a_workspace_that_is_no_tensor_is_named(workspace):
 def test_gather_of_more_positions_than_32_bits_is_named(n):
     with pytest.raises(ValueError, match="N must"):
         gather(args(), n=n)
+
+
+def test_paged_calls_run_in_the_library_that_is_loaded(monkeypatch):
+    """FLASHMASK_LIBRARY is read once: calls bound after a change of it still go to the library whose status
+    get_status() reads."""
+    from column_sparse_masked_b200 import paged
+
+    bound = []
+
+    class Binding:
+        @staticmethod
+        def bind(path):
+            bound.append(path)
+
+    loaded = fm.load_library()
+    monkeypatch.setenv("FLASHMASK_LIBRARY", "checks" if "checks" not in loaded._name else "")
+    monkeypatch.setattr(paged, "_calls", None)
+    monkeypatch.setitem(sys.modules, "column_sparse_masked_b200._paged_binding", Binding)
+    monkeypatch.setattr(fm, "_paged_binding", Binding, raising=False)
+    paged._load()
+    assert bound == [loaded._name]
