@@ -10,13 +10,16 @@ the static CUDA runtime (the library loads on hosts without a GPU driver).
 checks of mask values and scheduler indices that report FLASHMASK_ERR_BOUNDS.
 
 ``build_binding()`` compiles csrc/binding/paged_binding.cpp (host code, g++,
-against torch's headers) into _paged_binding.so, the marshalling of the
-paged-cache calls; ``build()`` brings it up to date as well.
+against torch's and Python's headers) into _paged_binding.so, the marshalling
+of the paged-cache calls from Python; ``build()`` brings it up to date as well
+where torch is installed.  The C library needs neither (``build_library()``, or
+``--library``).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -45,11 +48,26 @@ def _deps() -> list:
         [os.path.join(os.path.dirname(HERE), "include", "flashmask.h")]
 
 
-def build_binding(force: bool = False) -> str:
-    """Compiles (if stale) and returns the path of _paged_binding.so."""
+def _binding_key() -> str:
+    """What the binding is compiled against; it holds this text and refuses to load under another torch."""
+    import torch
+
+    return f"paged binding for torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_stale() -> bool:
+    """Whether _paged_binding.so is missing, older than its sources or compiled against another torch or Python."""
     header = os.path.join(os.path.dirname(HERE), "include", "flashmask.h")
     newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(header))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+    if not os.path.exists(BINDING) or os.path.getmtime(BINDING) < newest:
+        return True
+    with open(BINDING, "rb") as f:
+        return _binding_key().encode() + b"\0" not in f.read()
+
+
+def build_binding(force: bool = False) -> str:
+    """Compiles (if stale) and returns the path of _paged_binding.so."""
+    if not force and not binding_stale():
         return BINDING
     import torch
 
@@ -58,6 +76,7 @@ def build_binding(force: bool = False) -> str:
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DPAGED_BINDING_KEY="{_binding_key()}"', f'-DPAGED_BINDING_TORCH="{torch.__version__}"',
            *(f"-I{d}" for d in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"])),
            BINDING_SRC, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
@@ -70,7 +89,7 @@ def build_binding(force: bool = False) -> str:
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False, checks: bool = False) -> str:
+def build_library(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False, checks: bool = False) -> str:
     """Compiles (if stale) and returns the path of libflashmask.so (libflashmask_checks.so with
     checks=True)."""
     build_dir, lib = (BUILD_CHECKS, LIB_CHECKS) if checks else (BUILD, LIB)
@@ -107,10 +126,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, lib)
-    build_binding(force)
+    return lib
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False, checks: bool = False) -> str:
+    """build_library(), and the paged calls' binding where torch is installed."""
+    lib = build_library(force, verbose, ptxas_verbose, checks)
+    if importlib.util.find_spec("torch") is None:
+        sys.stderr.write("torch is not installed: the paged calls' Python binding is not built\n")
+    else:
+        build_binding(force)
     return lib
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose=True, ptxas_verbose="-v" in sys.argv,
-                checks="--checks" in sys.argv))
+    print((build_library if "--library" in sys.argv else build)(
+        force="--force" in sys.argv, verbose=True, ptxas_verbose="-v" in sys.argv, checks="--checks" in sys.argv))

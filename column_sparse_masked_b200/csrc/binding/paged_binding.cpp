@@ -13,6 +13,8 @@
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
+
 #include "../../../include/flashmask.h"
 
 namespace {
@@ -308,8 +310,20 @@ PyMethodDef methods[] = {
     {"bind", bind, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_binding", nullptr, -1, methods};
+const char key[] = PAGED_BINDING_KEY;
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_binding", key, -1, methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged_binding() { return PyModule_Create(&module); }
+// Tensors are read through torch's C++ layout, which another version need not share; loading under one
+// fails here, and the build finds the key in the file.
+PyMODINIT_FUNC PyInit__paged_binding() {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  const char* text = version ? PyUnicode_AsUTF8(version) : nullptr;
+  const bool same = text && std::strcmp(text, PAGED_BINDING_TORCH) == 0;
+  if (text && !same) PyErr_Format(PyExc_ImportError, "%s, not for torch %s", key, text);
+  Py_XDECREF(version);
+  Py_XDECREF(torch);
+  return same ? PyModule_Create(&module) : nullptr;
+}

@@ -19,6 +19,7 @@ tokens concerned left out.
 """
 from __future__ import annotations
 
+import importlib
 from typing import Optional, Tuple
 
 import torch
@@ -33,10 +34,13 @@ def _load():
     """The compiled marshalling of these calls (_paged_binding.so), bound to the library in use."""
     global _calls
     lib = load_library()
+    how = "build it with `python column_sparse_masked_b200/build.py"
     try:
-        from . import _paged_binding
+        _paged_binding = importlib.import_module("._paged_binding", __package__)
+    except ModuleNotFoundError as e:
+        raise RuntimeError(f"_paged_binding.so is missing: {how}`") from e
     except ImportError as e:
-        raise RuntimeError("_paged_binding.so is missing: build it with `python column_sparse_masked_b200/build.py`") from e
+        raise RuntimeError(f"_paged_binding.so does not load: {e}; {how} --force`") from e
     _paged_binding.bind(lib._name)
     _calls = _paged_binding
     return _calls
