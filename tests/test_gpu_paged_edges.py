@@ -119,3 +119,47 @@ def test_append_q_rows_whose_offsets_pass_31_bits():
     assert (buf[:lead] == 7).all()
     for a in range(0, Hq, 1 << 22):
         assert torch.equal(out[0, 0, a:a + (1 << 22)], row[0, 0].expand(min(1 << 22, Hq - a), d)), a
+
+
+# ---------------------------------------------------------------------------
+# attention: graphs at once, and the cap on CTAs
+# ---------------------------------------------------------------------------
+def sequences(seed, lens, bits, Hkv=2, d=128, width=None):
+    cache = Cache(seed, lens, Hkv, d, 64, bits, width=width).cuda()
+    g = torch.Generator().manual_seed(seed)
+    return cache, torch.randn(len(lens), 1, 4 * Hkv, d, generator=g).bfloat16().cuda(), i32(lens)
+
+
+def window(B, n, size):
+    """Causal windows of `size` keys, one mask head."""
+    j = torch.arange(n, dtype=torch.int32, device="cuda").expand(B, 1, n)
+    return [(j + size).contiguous(), torch.full_like(j, n + 1).contiguous(), None, None]
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("masked", [False, True])
+def test_graphs_on_their_own_streams_share_nothing(bits, masked):
+    """Two graphs with a memory pool each, replayed at the same time on two streams, give the bits of single calls in
+    every round."""
+    sets = []
+    for seed, lens in ((81, [3000, 50, 0]), (82, [10, 2100, 999])):
+        cache, q, n = sequences(seed, lens, bits)
+        vec = window(3, max(lens), 700) if masked else [None] * 4
+        call = (lambda q=q, c=cache, n=n, vec=vec: fm.paged_attention(q, c.k, c.v, c.table, n, *vec, **c.kw))
+        sets.append((call, call(), torch.cuda.Stream(), torch.cuda.CUDAGraph()))
+    torch.cuda.synchronize()
+    outs = []
+    for call, _, _, graph in sets:
+        with torch.cuda.graph(graph):
+            outs.append(call())
+    for _ in range(20):
+        for o, lse in outs:
+            o.fill_(7), lse.fill_(7)
+        torch.cuda.synchronize()
+        for _, _, stream, graph in sets:
+            with torch.cuda.stream(stream):
+                for _ in range(4):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for (o, lse), (_, (ro, rl), _, _) in zip(outs, sets):
+            assert torch.equal(o, ro) and torch.equal(lse, rl)
