@@ -411,9 +411,12 @@ void flashmask_set_wait_limit_ns(int64_t ns);
  * default, restores one CTA per SM).  With a small cap one CTA walks many
  * work items in a row, so tests can drive every item-to-item hand-over of the
  * persistent kernels (ring wrap-round, buffer hand-over, phase flips) on
- * problems small enough to check element by element.  Results do not depend
- * on the cap.  Host-side setting, process-wide; FLASHMASK_ERR_INVALID_ARG
- * for n < 0. */
+ * problems small enough to check element by element.  The results of fwd and
+ * bwd do not depend on the cap.  flashmask_paged_attention is capped where its
+ * warps take runs of tiles or whole items, not where it gives every item a CTA of
+ * its own; where items are cut, the cap moves the cuts and so the order in which
+ * O and LSE are summed (equal calls under one cap give equal bits).  Host-side
+ * setting, process-wide; FLASHMASK_ERR_INVALID_ARG for n < 0. */
 int flashmask_set_max_ctas(int32_t n);
 
 /* Launches one CTA whose only job is a bounded wait on a barrier that nothing

@@ -163,3 +163,26 @@ def test_graphs_on_their_own_streams_share_nothing(bits, masked):
         torch.cuda.synchronize()
         for (o, lse), (_, (ro, rl), _, _) in zip(outs, sets):
             assert torch.equal(o, ro) and torch.equal(lse, rl)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("lens,width,B,same", [([300, 90], None, 2, True), ([200, 17] * 80, None, 160, True),
+                                               ([5000, 300], 90, 2, False)])
+def test_the_cap_on_ctas_changes_the_order_of_sums_at_most(bits, lens, width, B, same):
+    """Items of one CTA and whole items of a warp give the same bits under any cap; items that are cut are cut
+    elsewhere, and their parts are joined in fp32."""
+    cache, q, n = sequences(83, lens, bits, width=width)
+    o, lse = fm.paged_attention(q, cache.k, cache.v, cache.table, n, **cache.kw)
+    try:
+        for cap in (1, 3, 40):
+            fm.set_max_ctas(cap)
+            o2, l2 = fm.paged_attention(q, cache.k, cache.v, cache.table, n, **cache.kw)
+            if same:
+                assert torch.equal(o, o2) and torch.equal(lse, l2)
+            # weights are rounded to bf16 against another running maximum, 2^-8 each on either side, and the
+            # result once more: 2^-8 (2 sum w |v| + 2 |o|), with |v| <= 5.5 (normal values, or -3 + 0.5 x 15)
+            assert (o.double() - o2.double()).abs().max() <= 4 * 2.0 ** -8 * 5.5
+            # fp32: 2^-20 covers exp2, log2 and the sums
+            assert ((lse.double() - l2.double()).abs() <= 2.0 ** -19 * (1 + lse.double().abs())).all()
+    finally:
+        fm.set_max_ctas(0)
