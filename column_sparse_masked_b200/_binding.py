@@ -335,7 +335,7 @@ def merge_partials(o_parts: Sequence[torch.Tensor], lse_parts: Sequence[torch.Te
 
 def set_max_ctas(n: int) -> None:
     """Caps the attention kernels' persistent grid at n CTAs (0 = one per SM); for tests.  Paged attention cuts long
-    items by the cap (another order of sums) and leaves the grid of one CTA per item as it is."""
+    items by the cap (other bits, within rounding) and leaves the grid of one CTA per item as it is."""
     _check(load_library().flashmask_set_max_ctas(int(n)), "flashmask_set_max_ctas")
 
 

@@ -98,7 +98,8 @@ PagedLayout paged_layout(const flashmask_pages& pg, const flashmask_paged_rows& 
   const bool masked = r.lts || r.uts;
   auto blocks = [&](int rows) { return (R + rows - 1) / rows; };
   // Rows of a block.  A block reads its keys once, so the fewest blocks read least; but blocks of 32 rows run
-  // with 4 warps an SM and a long way through cold instructions.  bf16, 32 rows over 32 sequences of 4K keys: blocks
+  // with 4 warps an SM, whose 128 accumulators a thread leave no room in 255 registers (156 bytes of stores and 144 of
+  // loads are spilled at d = 128), and a long way through cold instructions.  bf16, 32 rows over 32 sequences of 4K keys: blocks
   // of 32 take 145 us, of 16 188, of 8 331; over 8 sequences 59, 48 and 61; with masks that hide three
   // quarters 70, 61 and 76 over 32, 34, 30 and 30 over 8.  In 4 bits the codes' conversion counts and not the bytes: 32
   // rows over 32 sequences take 125 us in blocks of 16, 153 in blocks of 8 and 167 in blocks of 32.

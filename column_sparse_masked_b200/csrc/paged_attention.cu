@@ -46,9 +46,9 @@
 // Measured, heads of 128, 8 KV heads of 4 q-heads, one new token for each of 64 sequences of 256 to 8192 keys (262
 // thousand in all): bf16 98.6 us, 90 % of the measured copy bandwidth over the bytes that it cannot do
 // without; the rest is the chain lengths - pages - rows - tiles at the start, the merge, and SMs whose
-// bandwidth differs by 11 %.  In 4 bits 48.2 us, 46 %: the codes' conversion, 1400 instructions for 64 keys,
-// keeps half of the ALU pipe and of the issue slots busy with three warps a scheduler, which is as many as 168
-// registers allow.  A call of one tile takes 5.6 us: launch, the same chain, and code that is not in the
+// bandwidth differs by 11 %.  In 4 bits 48.4 us, 46 %, with no unit used up (issue slots and ALU pipe 50 %, memory
+// 38 %): 1400 instructions for 64 keys, most of them the codes' conversion, in one chain from conversion to scores
+// to softmax to values, and three warps a scheduler to overlap it, which is as many as 168 registers allow.  A call of one tile takes 5.6 us: launch, the same chain, and code that is not in the
 // instruction cache.
 #include <cuda_bf16.h>
 
@@ -783,6 +783,9 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, const CUtensorM
                   s[m2][nt][2 * hf + e] = pr;
                 }
               }
+              // Weights (4 bits: times the value's scale) are rounded to bf16, the type that the tensor cores take next to
+              // bf16 values, as in the dense forward; their sum takes them unrounded.  O is off by at most 2^-8
+              // sum w |v| so; against 64 bits 0.0019 to 0.0024 of its size, of which rounding O is 0.0016.
               pb[m2][nt][hf] = transpose8x8(pack_bf16x2(w[0], w[1]));
             }
         // ---- values that are not finite, in a tile that some row does not see whole ----
@@ -1394,8 +1397,8 @@ static cudaError_t launch_variant(const PagedAttnParams& p, const CUtensorMap& t
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || p.mode != kPagedSplit) return e;
-  // Runs of a CTA: 8 while all CTAs fit on the device at once (three an SM), else 16.  64 sequences of 4 rows: 98.0 us
-  // with 8, 99.7 with 16; 9 sequences of 32 rows 22.5 and 20.9.
+  // Runs of a CTA: 8 while all CTAs fit on the device at once (three an SM), else 16.  64 sequences of 4 rows: 98.4 us
+  // with 8, 100.0 with 16 (101.4 and 103.0 in a slower process); 9 sequences of 32 rows 22.5 and 20.9.
   const int workers = grid * C::kWarps, rows = std::min(C::kRows, p.Nq * p.G);
   const int runs = (workers + 7) / 8 * rows <= 3 * 148 ? 8 : 16;
   return launch_after(paged_merge_kernel<D, C::kRows>, dim3((workers + runs - 1) / runs, rows), dim3(256), 0, st, p, workers,

@@ -319,7 +319,8 @@ typedef struct flashmask_append {
  * c = cos[r][i], s = sin[r][i], where pair i is values (i, i + rot/2), or
  * (2i, 2i + 1) with `interleaved`.  The rotated q is written to q_out (rows at
  * or past counts[b] as 0), k and v into their pages; v is not rotated.
- * Rotated values are rounded once, to bf16.  With bits 4 each bf16 row x is
+ * Values are rotated in fp32 (bits 4: k to fp32's nearest) and rounded to
+ * bf16.  With bits 4 each bf16 row x is
  * stored as minimum = min x, scale = bf16((max x - min x) / 15) and the codes
  * nearest to (x - minimum) / scale (ties to even, at most 15); a row with a
  * NaN or an infinity, or whose spread overflows fp32, reads back as NaN.
@@ -356,8 +357,9 @@ typedef struct flashmask_paged_rows {
  * (NaN included).  With bits 4 the codes enter the products as they are
  * and the scales and minima are applied to sums in fp32.
  * Any Nq >= 0; a long chunk of rows is better served by flashmask_paged_gather
- * and flashmask_fwd.  The result does not depend on what other sequences hold
- * beyond fp32 summation order; equal calls give equal bits.
+ * and flashmask_fwd.  Other sequences of a call decide where an item is cut, and
+ * so the order of its fp32 sums and the running maximum against which a weight is
+ * rounded to bf16, and nothing else; equal calls give equal bits.
  */
 size_t flashmask_paged_attention_workspace_size(const flashmask_pages* pages, const flashmask_paged_rows* rows);
 int flashmask_paged_attention(const flashmask_pages* pages, const flashmask_paged_rows* rows, void* workspace,
@@ -414,8 +416,8 @@ void flashmask_set_wait_limit_ns(int64_t ns);
  * problems small enough to check element by element.  The results of fwd and
  * bwd do not depend on the cap.  flashmask_paged_attention is capped where its
  * warps take runs of tiles or whole items, not where it gives every item a CTA of
- * its own; where items are cut, the cap moves the cuts and so the order in which
- * O and LSE are summed (equal calls under one cap give equal bits).  Host-side
+ * its own; where items are cut, the cap moves the cuts and so, within its rounding,
+ * the result (equal calls under one cap give equal bits).  Host-side
  * setting, process-wide; FLASHMASK_ERR_INVALID_ARG for n < 0. */
 int flashmask_set_max_ctas(int32_t n);
 
