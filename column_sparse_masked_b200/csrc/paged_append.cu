@@ -84,9 +84,8 @@ __device__ __forceinline__ float code_of(float x, float lo, float scale, float i
   const float m = fmaf(diff, inv, 12582912.f), k = m - 12582912.f;  // to an integer, which is in m's low bits
   const float r = fmaf(-k, scale, diff);
   const float over = (fabsf(r) - half) + __uint_as_float(__float_as_uint(err) ^ (__float_as_uint(r) & 0x80000000u));
-  // an odd code gives way at the middle: over >= 0, written as over > the least number below 0
-  const float limit = __uint_as_float((__float_as_uint(m) & 1u) ? 0x80000001u : 0u);
-  return over > limit ? k + copysignf(1.f, r) : k;
+  // an odd code gives way at the middle too: there over is +0, whose bits and the code's last make 1
+  return __float_as_int(over) + (__float_as_int(m) & 1) > 0 ? k + copysignf(1.f, r) : k;
 }
 
 // Lower of two bf16 pairs, NaN if either is.
