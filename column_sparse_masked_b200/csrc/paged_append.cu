@@ -100,7 +100,8 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
 // `gpt` apart with that token's cosines and sines in registers.
 // Bound by memory for bf16 (8192 tokens of 48 rows: 36.6 us, 86 % of the measured copy bandwidth).
 // 4 bits are bound by issue and latency together (60 % of the issue slots busy): 64 registers, for 32 warps an
-// SM, take 41.6 us with the gather of 9 ragged prompts, 72 registers 43.8, 56 with a few spilled 41.9, 48 44.4.
+// SM, take 41.6 us with the gather of 9 ragged prompts, 72 registers 43.8, 56 with a few spilled 41.9, 48 44.4 (40.7 with 64
+// since the codes are decided as they are now).
 template <int D, int BITS>
 __global__ void __launch_bounds__(128, BITS == 4 ? 8 : 1) paged_append_kernel(AppendParams p, int gpt_log2) {
   constexpr int L = D / 16;
@@ -315,7 +316,7 @@ cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st) {
   const int L = p.pg.d / 16, rows = (p.q ? p.Hq : 0) + 2 * p.pg.Hkv;
   // Lane groups per token (log2).  Few groups share a token's place and angles among many rows (8192 tokens of
   // 48 bf16 rows: 4 groups 36.6 us, 8 groups 37.4, 16 groups 38.7; rows stored in 4 bits take longer each, and
-  // 8 groups are best: 41.6 us with the gather; at 72 registers 43.4 against 47.7 with 4 and 43.6 with 16); a
+  // 8 groups are best: 40.7 us with the gather; at 72 registers 43.4 against 47.7 with 4 and 43.6 with 16); a
   // small call spreads over the device, at most one group a row.
   int gl = 0;
   while ((1 << gl) < rows && (1 << gl) < 128 / L && (gl < (p.pg.bits == 4 ? 3 : 2) || (tokens << gl) * L / 32 < 148 * 32)) ++gl;

@@ -44,11 +44,11 @@
 //    e4m3 issues every 21 clocks, m16n8k16 in bf16 every 8.5.
 //
 // Measured, heads of 128, 8 KV heads of 4 q-heads, one new token for each of 64 sequences of 256 to 8192 keys (262
-// thousand in all): bf16 98.6 us, 90 % of the measured copy bandwidth over the bytes that it cannot do
+// thousand in all): bf16 99 us, 89 % of the measured copy bandwidth over the bytes that it cannot do
 // without; the rest is the chain lengths - pages - rows - tiles at the start, the merge, and SMs whose
-// bandwidth differs by 11 %.  In 4 bits 48.4 us, 46 %, with no unit used up (issue slots and ALU pipe 50 %, memory
+// bandwidth differs by 11 %.  In 4 bits 48.6 us, 45 %, with no unit used up (issue slots and ALU pipe 50 %, memory
 // 38 %): 1400 instructions for 64 keys, most of them the codes' conversion, in one chain from conversion to scores
-// to softmax to values, and three warps a scheduler to overlap it, which is as many as 168 registers allow.  A call of one tile takes 5.6 us: launch, the same chain, and code that is not in the
+// to softmax to values, and three warps a scheduler to overlap it, which is as many as 168 registers allow.  A call of one tile takes 5.8 us: launch, the same chain, and code that is not in the
 // instruction cache.
 #include <cuda_bf16.h>
 
