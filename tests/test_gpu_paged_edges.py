@@ -1,6 +1,6 @@
 """Paged key/value cache on the GPU, at values, outputs and calls that tests/test_gpu_paged.py does not reach: codes
-whose exact quotient lies beside the middle of two codes by less than fp32 sees, and outputs inside the caller's
-buffers."""
+whose exact quotient lies beside the middle of two codes by less than fp32 sees, outputs inside the caller's buffers,
+offsets past 31 bits, graphs replayed at the same time, and the cap on CTAs."""
 from fractions import Fraction
 
 import numpy as np
