@@ -13,7 +13,8 @@ plain tensors, ``k_pages`` and ``v_pages``:
 sequence b is slot ``j % page_size`` of page ``block_table[b, j // page_size]``.
 The calls run on the current stream of the tensors' device, allocate only
 their outputs and workspace (or take them), never synchronise and can be
-captured in a CUDA graph.  They record no gradient.  Table entries, positions
+captured in a CUDA graph.  They record no gradient.  Tensors are contiguous and
+16-byte aligned (a workspace: 256 bytes) where nothing else is said.  Table entries, positions
 and lengths out of range are reported by ``get_status()`` (-9), with the
 tokens concerned left out.
 """
